@@ -160,7 +160,7 @@ def prepare(case, seed):
         if own:
             moe, _ = _library()
             cfg = moe.LayerCfg(d=256, f=128, E=E, k=k, renorm=int(case["renorm"]))
-            s |= {"cfg": cfg, "ws": moe.balance_workspace(cfg, T), "stats": torch.empty(4, device="cuda"),
+            s |= {"cfg": cfg, "ws": moe.balance_workspace(cfg), "stats": torch.empty(4, device="cuda"),
                   "counts": torch.empty(E, dtype=torch.int32, device="cuda"), "prob": torch.empty(E, device="cuda"),
                   "d_logits": torch.empty(T, E, device="cuda")}
         return s
