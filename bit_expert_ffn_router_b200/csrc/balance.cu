@@ -1,0 +1,458 @@
+// The router's balance loss with its per-expert counts, and the gradient of
+// the router's logits.
+//
+// Over the n tokens that count (mask byte set, at least one logit above
+// -infinity), with p_t = softmax(l_t) over the E logits, c_e the (token, j)
+// choices of expert e and S_e = sum_t p_te:
+//   balance = E / (k n) * sum_e c_e * S_e / n,     z = sum_t lse_t^2 / n,
+//   lse_t = log sum_e exp(l_te).
+// The counts are whole numbers and take no gradient, so with the upstream
+// gradients a of balance and b of z
+//   d l_te = p_te * (a E / (k n^2) * (c_e - sum_i c_i p_ti) + b 2/n lse_t)
+//            + the gates' part.
+// Gates g_j over the k choices (softmax over the chosen logits, renorm) give
+// g_j (dg_j - sum_i g_i dg_i) at the chosen experts; gates read from the full
+// softmax give g_j dg_j there and -p_te sum_i g_i dg_i at every expert.
+//
+// Each direction reads the logits once (a token's row lives in the registers
+// of a lane group: its maximum, sum and weighted sum are shuffles) and the
+// backward pass writes the gradient once; p is recomputed rather than kept,
+// since an exponential costs less than eight more bytes per logit. Rows: 4 to
+// 32 lanes by E, 1 to 8 float4 per lane, so short rows share a warp.
+//
+// Sums over tokens: a lane adds its own experts' p over its rows in fp32 (one
+// CTA of 2 per SM sees T / 296 rows at most beyond the smallest T), the CTA
+// adds its lane groups in a fixed order, and the finish adds the CTAs'
+// partial sums in fp64, in a fixed order too: results do not depend on the
+// timing. The counts are integer atomics in shared memory.
+#include <cooperative_groups.h>
+
+#include <type_traits>
+
+#include "moe_internal.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kBThreads = 512;
+constexpr int kBWarps = kBThreads / 32;
+constexpr int kFinCtas = 8;  // CTAs of the finish: one cluster
+
+struct BalanceRows {
+  const float* logits;
+  const int32_t* idx;
+  const float* gate;
+  const uint8_t* mask;  // or null
+  int T, E, k;
+  int* status;
+};
+
+struct BalanceOut {
+  float* stats;     // balance, z, tokens, largest load
+  int32_t* counts;  // [E]
+  float* prob;      // [E]
+};
+
+// A token's row in a lane group: slot (i, c) of lane s holds expert
+// (i * LANES + s) * 4 + c; slots past E hold -infinity.
+template <int LANES, int SLOTS>
+struct Row {
+  float v[SLOTS * 4];
+
+  __device__ __forceinline__ static int expert(int i, int sub) { return (i * LANES + sub) * 4; }
+
+  __device__ __forceinline__ void load(const float* __restrict__ p, int E, int sub, bool vec) {
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      const int e = expert(i, sub);
+      if (vec) {
+        float4 a = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (e < E) a = __ldg(reinterpret_cast<const float4*>(p + e));
+        v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[4 * i + c] = e + c < E ? __ldg(p + e + c) : -INFINITY;
+      }
+    }
+  }
+
+  // v <- exp(v - max); returns the sum (0: nothing above -infinity; NaN if
+  // the row holds one) and the maximum.
+  __device__ __forceinline__ float exp_sum(float& m) {
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < SLOTS * 4; ++i) m = fmaxf(m, v[i]);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < SLOTS * 4; ++i) {
+      v[i] = __expf(v[i] - base);
+      s += v[i];
+    }
+    return group_sum(s, LANES);
+  }
+};
+
+// Adds up what the CTAs left behind; one cluster, CTA r finishes the experts
+// [r * per, r * per + per). With one CTA of rows the caller passes its own
+// sums (n_parts = 1) and a grid of one.
+struct Partials {
+  float* sum;    // [n][E]
+  int32_t* cnt;  // [n][E]
+  double* z;     // [n]
+  int32_t* tok;  // [n]
+};
+
+__device__ __forceinline__ double block_sum(double v, double* scratch) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double t = 0;
+  for (int i = 0; i < kBWarps; ++i) t += scratch[i];
+  return t;
+}
+
+__device__ __forceinline__ int block_max(int v, int* scratch) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int t = 0;
+  for (int i = 0; i < kBWarps; ++i) t = max(t, scratch[i]);
+  return t;
+}
+
+// stats from the sums over all experts; one thread.
+__device__ __forceinline__ void write_stats(float* stats, double dot, double z, int n, int top, int E, int k) {
+  const double m = n > 0 ? n : 1;
+  stats[0] = static_cast<float>(dot * E / (k * m * m));
+  stats[1] = static_cast<float>(z / m);
+  stats[2] = static_cast<float>(n);
+  stats[3] = static_cast<float>(static_cast<double>(top) * E / (k * m));
+}
+
+template <int LANES, int SLOTS>
+__global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O, bool vec) {
+  extern __shared__ float sums[];  // [kBWarps][E]
+  __shared__ int hist[kMaxE];
+  __shared__ double scratch[kBWarps];
+  __shared__ int iscratch[kBWarps];
+  constexpr int kRows = 32 / LANES;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
+  const int E = R.E, k = R.k;
+  for (int e = threadIdx.x; e < E; e += kBThreads) hist[e] = 0;
+  __syncthreads();
+
+  float acc[SLOTS * 4];
+#pragma unroll
+  for (int i = 0; i < SLOTS * 4; ++i) acc[i] = 0.f;
+  double z = 0;
+  int n = 0;
+  const int stride = gridDim.x * kBWarps * kRows;
+  // every lane of a warp makes the same number of turns: the shuffles are warp-wide
+  for (int t0 = (blockIdx.x * kBWarps + warp) * kRows; t0 < R.T; t0 += stride) {
+    const int t = t0 + lane / LANES;
+    const bool in = t < R.T && (R.mask == nullptr || __ldg(R.mask + t) != 0);
+    Row<LANES, SLOTS> row;
+    row.load(R.logits + static_cast<size_t>(in ? t : 0) * E, E, sub, vec);
+    float m;
+    const float s = row.exp_sum(m);
+    if (!in || s == 0.f) continue;
+    const float r = 1.f / s;
+#pragma unroll
+    for (int i = 0; i < SLOTS * 4; ++i) acc[i] += row.v[i] * r;
+    if (sub == 0) {
+      const float lse = m + logf(s);
+      z += static_cast<double>(lse) * lse;
+      ++n;
+    }
+    for (int j = sub; j < k; j += LANES) {
+      const int e = __ldg(R.idx + static_cast<size_t>(t) * k + j);
+      if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
+        atomicAdd(&hist[e], 1);
+      else
+        report(R.status, kDevBadExpert, t * k + j);
+    }
+  }
+  // lane groups of a warp, then the warps
+#pragma unroll
+  for (int i = 0; i < SLOTS * 4; ++i) {
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    const int e = Row<LANES, SLOTS>::expert(i / 4, sub) + i % 4;
+    if (lane < LANES && e < E) sums[warp * E + e] = acc[i];
+  }
+  z = block_sum(z, scratch);  // its barriers also publish sums and hist
+  n = static_cast<int>(block_sum(static_cast<double>(n), scratch));
+  if (gridDim.x > 1) {
+    for (int e = threadIdx.x; e < E; e += kBThreads) {
+      float s = 0.f;
+      for (int w = 0; w < kBWarps; ++w) s += sums[w * E + e];
+      P.sum[static_cast<size_t>(blockIdx.x) * E + e] = s;
+      P.cnt[static_cast<size_t>(blockIdx.x) * E + e] = hist[e];
+    }
+    if (threadIdx.x == 0) {
+      P.z[blockIdx.x] = z;
+      P.tok[blockIdx.x] = n;
+    }
+    return;
+  }
+  // all rows were this CTA's: finish here
+  double dot = 0;
+  int top = 0;
+  for (int e = threadIdx.x; e < E; e += kBThreads) {
+    double s = 0;
+    for (int w = 0; w < kBWarps; ++w) s += sums[w * E + e];
+    dot += s * hist[e];
+    top = max(top, hist[e]);
+    O.prob[e] = static_cast<float>(s / max(n, 1));
+    O.counts[e] = hist[e];
+  }
+  dot = block_sum(dot, scratch);
+  top = block_max(top, iscratch);
+  if (threadIdx.x == 0) write_stats(O.stats, dot, z, n, top, E, k);
+}
+
+// The finish over n_parts CTAs' sums: a cluster of kFinCtas CTAs, each over
+// its share of the experts; a warp takes 32 experts of one sixteenth of the
+// parts (coalesced rows), the CTA adds its warps, and CTA 0 adds the CTAs'
+// scalars through distributed shared memory.
+__global__ void __cluster_dims__(kFinCtas) __launch_bounds__(kBThreads)
+    balance_finish_kernel(Partials P, BalanceOut O, int n_parts, int E, int k) {
+  __shared__ double part[kBWarps][32];
+  __shared__ int partc[kBWarps][32];
+  __shared__ double scratch[kBWarps];
+  __shared__ int iscratch[kBWarps];
+  __shared__ double share_dot;
+  __shared__ int share_top;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
+  double z = 0, tok = 0;
+  for (int i = threadIdx.x; i < n_parts; i += kBThreads) {
+    z += P.z[i];
+    tok += P.tok[i];
+  }
+  z = block_sum(z, scratch);
+  const int n = static_cast<int>(block_sum(tok, scratch));
+  double dot = 0;
+  int top = 0;
+  for (int e0 = blockIdx.x * 32; e0 < E; e0 += kFinCtas * 32) {
+    const int e = e0 + lane;
+    double s = 0;
+    int c = 0;
+    if (e < E)
+      for (int i = warp; i < n_parts; i += kBWarps) {
+        s += P.sum[static_cast<size_t>(i) * E + e];
+        c += P.cnt[static_cast<size_t>(i) * E + e];
+      }
+    part[warp][lane] = s;
+    partc[warp][lane] = c;
+    __syncthreads();
+    if (warp == 0 && e < E) {
+      for (int w = 1; w < kBWarps; ++w) {
+        s += part[w][lane];
+        c += partc[w][lane];
+      }
+      dot += s * c;
+      top = max(top, c);
+      O.prob[e] = static_cast<float>(s / max(n, 1));
+      O.counts[e] = c;
+    }
+    __syncthreads();
+  }
+  dot = block_sum(dot, scratch);
+  top = block_max(top, iscratch);
+  if (threadIdx.x == 0) {
+    share_dot = dot;
+    share_top = top;
+  }
+  cluster.sync();
+  if (cluster.block_rank() == 0 && threadIdx.x == 0) {
+    for (int r = 1; r < kFinCtas; ++r) {
+      dot += *cluster.map_shared_rank(&share_dot, r);
+      top = max(top, *cluster.map_shared_rank(&share_top, r));
+    }
+    write_stats(O.stats, dot, z, n, top, E, k);
+  }
+  cluster.sync();  // the others' shared memory stays until it has been read
+}
+
+template <int LANES, int SLOTS>
+__global__ void __launch_bounds__(kBThreads)
+    balance_backward_kernel(BalanceRows R, const float* __restrict__ stats, const int32_t* __restrict__ counts,
+                            const float* __restrict__ d_loss, const float* __restrict__ d_gate, bool renorm, bool vec,
+                            float* __restrict__ d_logits) {
+  constexpr int kRows = 32 / LANES;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
+  const int E = R.E, k = R.k;
+  const float n = fmaxf(__ldg(stats + 2), 1.f);
+  const float ca = __ldg(d_loss) * (static_cast<float>(E) / k) / n / n;
+  const float cz = __ldg(d_loss + 1) * 2.f / n;
+  float c[SLOTS * 4];  // ca * counts of this lane's experts
+#pragma unroll
+  for (int i = 0; i < SLOTS * 4; ++i) {
+    const int e = Row<LANES, SLOTS>::expert(i / 4, sub) + i % 4;
+    c[i] = e < E ? ca * __ldg(counts + e) : 0.f;
+  }
+  const int stride = gridDim.x * kBWarps * kRows;
+  for (int t0 = (blockIdx.x * kBWarps + warp) * kRows; t0 < R.T; t0 += stride) {
+    const int t = t0 + lane / LANES;
+    const bool live = t < R.T;
+    const bool in = live && (R.mask == nullptr || __ldg(R.mask + t) != 0);
+    Row<LANES, SLOTS> row;
+    row.load(R.logits + static_cast<size_t>(in ? t : 0) * E, E, sub, vec);
+    float m;
+    const float s = row.exp_sum(m);
+    const bool keep = in && s != 0.f;
+    const float r = 1.f / s;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < SLOTS * 4; ++i) dot += row.v[i] * c[i];
+    dot = group_sum(dot, LANES) * r;
+    // the gates' weighted sum
+    const int32_t* ti = R.idx + static_cast<size_t>(live ? t : 0) * k;
+    const float* tg = R.gate + static_cast<size_t>(live ? t : 0) * k;
+    const float* td = d_gate + static_cast<size_t>(live ? t : 0) * k;
+    float gs = 0.f;
+    if (d_gate != nullptr) {
+      for (int j = sub; j < k; j += LANES) gs += __ldg(tg + j) * __ldg(td + j);
+      gs = group_sum(gs, LANES);
+    }
+    // every expert: p * (c_e + base); a z gradient of 0 leaves an infinite lse out
+    const float base = (cz != 0.f ? cz * (m + logf(s)) : 0.f) - dot - (renorm ? 0.f : gs);
+    if (live) {
+      float* out = d_logits + static_cast<size_t>(t) * E;
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) {
+        const int e = Row<LANES, SLOTS>::expert(i, sub);
+        float o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = keep ? row.v[4 * i + q] * r * (c[4 * i + q] + base) : 0.f;
+        if (vec) {
+          if (e < E) *reinterpret_cast<float4*>(out + e) = make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (e + q < E) out[e + q] = o[q];
+        }
+      }
+    }
+    __syncwarp();  // the stores above come before the chosen experts' below
+    if (d_gate != nullptr && keep) {
+      float* out = d_logits + static_cast<size_t>(t) * E;
+      const float mm = m;
+      for (int j = sub; j < k; j += LANES) {
+        const int e = __ldg(ti + j);
+        if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) continue;
+        // an expert named more than once takes the sum of its parts, in rank
+        // order, from each of the lanes that store it
+        float part = 0.f;
+        for (int i = 0; i < k; ++i) {
+          if (__ldg(ti + i) != e) continue;
+          part += __ldg(tg + i) * (__ldg(td + i) - (renorm ? gs : 0.f));
+        }
+        const float p = __expf(__ldg(R.logits + static_cast<size_t>(t) * E + e) - mm) * r;
+        out[e] = p * (ca * __ldg(counts + e) + base) + part;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+bool rows_vec(const void* p, int E) { return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Lanes of a row and float4 per lane, by E.
+template <typename F>
+cudaError_t by_experts(int E, F f) {
+  using std::integral_constant;
+  if (E <= 16) return f(integral_constant<int, 4>(), integral_constant<int, 1>());
+  if (E <= 32) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
+  if (E <= 64) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
+  if (E <= 128) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
+  if (E <= 256) return f(integral_constant<int, 32>(), integral_constant<int, 2>());
+  if (E <= 512) return f(integral_constant<int, 32>(), integral_constant<int, 4>());
+  return f(integral_constant<int, 32>(), integral_constant<int, 8>());
+}
+
+int rows_per_warp(int E) { return E <= 16 ? 8 : E <= 32 ? 4 : E <= 64 ? 2 : 1; }
+
+// One CTA while each of its lane groups has at most kOneCta rows, else up to
+// two CTAs per SM.
+constexpr int kOneCta = 4;
+
+int balance_ctas(const Ctx& ctx, int E, int T) {
+  const int per_cta = kBWarps * rows_per_warp(E);
+  if (T <= per_cta * kOneCta) return 1;
+  const int want = (T + per_cta - 1) / per_cta;
+  const int most = 2 * ctx.num_sms < kBalanceMaxCtas ? 2 * ctx.num_sms : kBalanceMaxCtas;
+  return want < most ? want : most;
+}
+
+}  // namespace
+
+size_t balance_ws_bytes(int E) {
+  return static_cast<size_t>(kBalanceMaxCtas) * (static_cast<size_t>(E) * 8 + 16) + 1024;
+}
+
+cudaError_t balance_init(const Ctx& ctx) {
+  (void)ctx;
+  return cudaFuncSetAttribute(balance_rows_kernel<32, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kBWarps * kMaxE * 4);
+}
+
+cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
+                           const uint8_t* mask, int T, float* stats, int32_t* counts, float* prob, void* ws,
+                           cudaStream_t s) {
+  const int E = c.E, n = T > 0 ? balance_ctas(ctx, E, T) : 1;
+  const BalanceRows R{logits, idx, nullptr, mask, T, E, c.k, ctx.d_status};
+  const BalanceOut O{stats, counts, prob};
+  char* b = static_cast<char*>(ws);
+  Partials P;
+  P.z = reinterpret_cast<double*>(b);
+  P.sum = reinterpret_cast<float*>(P.z + kBalanceMaxCtas);
+  P.cnt = reinterpret_cast<int32_t*>(P.sum + static_cast<size_t>(kBalanceMaxCtas) * E);
+  P.tok = P.cnt + static_cast<size_t>(kBalanceMaxCtas) * E;
+  const bool vec = rows_vec(logits, E);
+  const cudaError_t e = by_experts(E, [&](auto lanes, auto slots) {
+    balance_rows_kernel<lanes.value, slots.value><<<n, kBThreads, kBWarps * E * 4, s>>>(R, P, O, vec);
+    return cudaGetLastError();
+  });
+  if (e != cudaSuccess || n == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kFinCtas);
+  cfg.blockDim = dim3(kBThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, balance_finish_kernel, P, O, n, E, c.k);
+}
+
+cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
+                                    const float* gate, const uint8_t* mask, int T, const float* stats,
+                                    const int32_t* counts, const float* d_loss, const float* d_gate, float* d_logits,
+                                    cudaStream_t s) {
+  const int E = c.E;
+  const BalanceRows R{logits, idx, gate, mask, T, E, c.k, ctx.d_status};
+  const bool vec = rows_vec(logits, E) && rows_vec(d_logits, E);
+  const int per_cta = kBWarps * rows_per_warp(E);
+  const int want = (T + per_cta - 1) / per_cta;
+  const int n = want < 2 * ctx.num_sms ? want : 2 * ctx.num_sms;
+  return by_experts(E, [&](auto lanes, auto slots) {
+    balance_backward_kernel<lanes.value, slots.value><<<n, kBThreads, 0, s>>>(R, stats, counts, d_loss, d_gate,
+                                                                            c.renorm != 0, vec, d_logits);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace moe

@@ -155,6 +155,22 @@ static moe_status check_pool(const moe_layer_cfg& c, const uint8_t* pool, size_t
   return MOE_OK;
 }
 
+// Sizes of an MX matrix; the block grid of the conversions has to fit.
+static moe_status check_mx4(int rows, int cols) {
+  if (rows < 0 || cols <= 0) return MOE_EINVAL;
+  if (cols % kBlock != 0 || cols > kMx4MaxCols) return MOE_EUNSUPPORTED;
+  return static_cast<long long>(rows) * (cols / 8) <= (1ll << 40) ? MOE_OK : MOE_EUNSUPPORTED;
+}
+
+static size_t type_size(int type) {
+  switch (type) {
+    case MOE_TYPE_BF16:
+    case MOE_TYPE_FP16: return 2;
+    case MOE_TYPE_FP32: return 4;
+    default: return 0;
+  }
+}
+
 static moe_status fill_grouping(const moe_layer_cfg& c, int T, void* ws, moe_grouping* out) {
   const WsLayout w = ws_layout(c, T);
   const GroupPtrs g = group_ptrs(c, T, ws);
@@ -315,7 +331,8 @@ moe_status moe_ctx_create(int device, moe_ctx** out) {
     }
   }
   if (cudaMemset(ctx->c.d_status, 0, 64) != cudaSuccess || router_init(ctx->c) != cudaSuccess || router_tc_init(ctx->c) != cudaSuccess ||
-      decode_init(ctx->c) != cudaSuccess || prefill_init(ctx->c) != cudaSuccess) {
+      decode_init(ctx->c) != cudaSuccess || prefill_init(ctx->c) != cudaSuccess ||
+      balance_init(ctx->c) != cudaSuccess || mx4_product_init(ctx->c) != cudaSuccess) {
     cudaFree(ctx->c.d_status);
     delete ctx;
     return MOE_ECUDA;
@@ -624,6 +641,140 @@ moe_status moe_layer_forward(moe_ctx* ctx, const moe_layer_cfg* cfg, const void*
                     nullptr, stream)) != MOE_OK)
     return st;
   return moe_combine(ctx, cfg, &g, z, x, T, y, stream);
+}
+
+// The calls below look at every argument before they touch the device.
+
+size_t moe_balance_workspace_bytes(const moe_layer_cfg* cfg) {
+  return check_cfg(cfg) == MOE_OK ? balance_ws_bytes(cfg->E) : 0;
+}
+
+moe_status moe_balance_loss(moe_ctx* ctx, const moe_layer_cfg* cfg, const float* logits, const int32_t* idx,
+                            const uint8_t* mask, int T, float* stats, int32_t* counts, float* prob, void* ws,
+                            size_t ws_bytes, moe_stream stream) {
+  if (ctx == nullptr) return MOE_EINVAL;
+  const moe_status st = check_cfg_unskipped(cfg);
+  if (st != MOE_OK) return st;
+  if (T < 0 || stats == nullptr || counts == nullptr || prob == nullptr) return MOE_EINVAL;
+  if (!aligned(stats, 4) || !aligned(counts, 4) || !aligned(prob, 4)) return MOE_EINVAL;
+  if (T > 0 && (logits == nullptr || idx == nullptr || !aligned(logits, 4) || !aligned(idx, 4))) return MOE_EINVAL;
+  if (ws == nullptr || !aligned(ws, 256)) return MOE_EINVAL;
+  if (ws_bytes < balance_ws_bytes(cfg->E)) return MOE_ENOSPACE;
+  DeviceGuard dg(ctx->c.device);
+  if (!dg.ok) return MOE_ECUDA;
+  return from_cuda(launch_balance(ctx->c, *cfg, logits, idx, mask, T, stats, counts, prob, ws,
+                                  static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_balance_loss_backward(moe_ctx* ctx, const moe_layer_cfg* cfg, const float* logits, const int32_t* idx,
+                                     const float* gate, const uint8_t* mask, int T, const float* stats,
+                                     const int32_t* counts, const float* d_loss, const float* d_gate, float* d_logits,
+                                     moe_stream stream) {
+  if (ctx == nullptr) return MOE_EINVAL;
+  const moe_status st = check_cfg_unskipped(cfg);
+  if (st != MOE_OK) return st;
+  if (T < 0) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (logits == nullptr || idx == nullptr || stats == nullptr || counts == nullptr || d_loss == nullptr ||
+      d_logits == nullptr || (d_gate != nullptr && gate == nullptr))
+    return MOE_EINVAL;
+  const void* ptrs[] = {logits, idx, gate, stats, counts, d_loss, d_gate, d_logits};
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return MOE_EINVAL;
+  DeviceGuard dg(ctx->c.device);
+  if (!dg.ok) return MOE_ECUDA;
+  return from_cuda(launch_balance_backward(ctx->c, *cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate,
+                                           d_logits, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_mx4_scale_pitch(int cols) {
+  return check_mx4(0, cols) == MOE_OK ? static_cast<size_t>(mx4_pitch(cols)) : 0;
+}
+
+moe_status moe_mx4_quantize(moe_ctx* ctx, const void* x, int x_type, int rows, int cols, size_t ld, uint8_t* codes,
+                            uint8_t* scales, moe_stream stream) {
+  if (ctx == nullptr) return MOE_EINVAL;
+  const moe_status st = check_mx4(rows, cols);
+  if (st != MOE_OK) return st;
+  if (type_size(x_type) == 0) return MOE_EUNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (x == nullptr || !aligned(x, type_size(x_type)) || (rows > 1 && ld < static_cast<size_t>(cols)))
+    return MOE_EINVAL;
+  if (codes == nullptr || scales == nullptr || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_EINVAL;
+  DeviceGuard dg(ctx->c.device);
+  if (!dg.ok) return MOE_ECUDA;
+  return from_cuda(
+      launch_mx4_quantize(x, x_type, rows, cols, ld, codes, scales, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_mx4_dequantize(moe_ctx* ctx, const uint8_t* codes, const uint8_t* scales, int rows, int cols, void* out,
+                              int out_type, size_t ld, moe_stream stream) {
+  if (ctx == nullptr) return MOE_EINVAL;
+  const moe_status st = check_mx4(rows, cols);
+  if (st != MOE_OK) return st;
+  if (type_size(out_type) == 0) return MOE_EUNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (out == nullptr || !aligned(out, type_size(out_type)) || (rows > 1 && ld < static_cast<size_t>(cols)))
+    return MOE_EINVAL;
+  if (codes == nullptr || scales == nullptr || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_EINVAL;
+  DeviceGuard dg(ctx->c.device);
+  if (!dg.ok) return MOE_ECUDA;
+  return from_cuda(
+      launch_mx4_dequantize(codes, scales, rows, cols, out, out_type, ld, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_mx4_product(moe_ctx* ctx, const uint8_t* x_codes, const uint8_t* x_scales, int x_rows,
+                           const moe_mx4_matrix* w, const moe_grouping* grouping, int shared_slot, int flags,
+                           void* out, int out_type, size_t ld, moe_stream stream) {
+  if (ctx == nullptr || w == nullptr) return MOE_EINVAL;
+  moe_status st = check_mx4(x_rows, w->cols);
+  if (st != MOE_OK) return st;
+  if (w->rows <= 0 || w->n_slots <= 0) return MOE_EINVAL;
+  if (w->rows % 16 != 0 || type_size(out_type) == 0) return MOE_EUNSUPPORTED;
+  if ((flags & ~(MOE_MX4_GATHER | MOE_MX4_SWIGLU | MOE_MX4_GATE)) != 0) return MOE_EINVAL;
+  if (w->codes == nullptr || w->scales == nullptr || !aligned(w->codes, 16) || !aligned(w->scales, 16))
+    return MOE_EINVAL;
+  if (w->n_slots > 1) {
+    const size_t rows = static_cast<size_t>(w->rows);
+    if (w->code_stride % 16 != 0 || w->code_stride < rows * (w->cols / 2) || w->scale_stride % 16 != 0 ||
+        w->scale_stride < rows * mx4_pitch(w->cols))
+      return MOE_EINVAL;
+  }
+  long long out_rows = x_rows;
+  if (grouping == nullptr) {
+    if (shared_slot != -1 || (flags & (MOE_MX4_GATHER | MOE_MX4_GATE)) != 0) return MOE_EINVAL;
+  } else {
+    const moe_grouping& g = *grouping;
+    if (g.T < 0 || g.k <= 0 || g.k > kMaxK || g.E <= 0 || g.E > kMaxE || g.n_pairs != g.T * g.k) return MOE_EINVAL;
+    if (shared_slot < -1 || shared_slot >= w->n_slots) return MOE_EINVAL;
+    out_rows = static_cast<long long>(g.n_pairs) + (shared_slot >= 0 ? g.T : 0);
+    if ((flags & MOE_MX4_GATHER) != 0 ? x_rows != g.T : x_rows < out_rows) return MOE_EINVAL;
+    if (g.T > 0 && (g.uniq_slot == nullptr || g.uniq_offset == nullptr || g.n_uniq == nullptr ||
+                    g.pair_token == nullptr || g.pair_gate == nullptr))
+      return MOE_EINVAL;
+  }
+  if (out_rows == 0) return MOE_OK;
+  if (x_codes == nullptr || x_scales == nullptr || !aligned(x_codes, 16) || !aligned(x_scales, 16)) return MOE_EINVAL;
+  const size_t out_cols = static_cast<size_t>((flags & MOE_MX4_SWIGLU) != 0 ? w->rows / 2 : w->rows);
+  if (out == nullptr || !aligned(out, type_size(out_type)) || (out_rows > 1 && ld < out_cols)) return MOE_EINVAL;
+  Mx4Args a;
+  a.x_codes = x_codes;
+  a.x_scales = x_scales;
+  a.x_rows = x_rows;
+  a.w = *w;
+  a.g = grouping;
+  a.shared_slot = shared_slot;
+  a.gather = (flags & MOE_MX4_GATHER) != 0;
+  a.swiglu = (flags & MOE_MX4_SWIGLU) != 0;
+  a.gate = (flags & MOE_MX4_GATE) != 0;
+  a.out = out;
+  a.out_type = out_type;
+  a.ld = ld;
+  DeviceGuard dg(ctx->c.device);
+  if (!dg.ok) return MOE_ECUDA;
+  const cudaError_t e = launch_mx4_product(ctx->c, a, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return MOE_EUNSUPPORTED;
+  return from_cuda(e);
 }
 
 }  // extern "C"

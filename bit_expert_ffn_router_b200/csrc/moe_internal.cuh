@@ -19,6 +19,8 @@ constexpr int kMaxK = 32;             // experts per token
 constexpr int kSlotAbsent = -1;       // slot-table value of an expert this device does not hold
 constexpr int kGroupChunk = 512;      // pairs per chunk in the multi-CTA grouping
 constexpr int kTileN = 128;           // tokens per tile of the prefill grouped GEMM
+constexpr int kBalanceMaxCtas = 320;  // CTAs whose partial sums the balance loss keeps in its workspace
+constexpr int kMx4MaxCols = 65536;    // values of a row of an MX matrix
 
 // Device status word codes (word 0 holds the first error seen).
 constexpr int kDevBadExpert = 1;
@@ -225,6 +227,39 @@ cudaError_t launch_usage_count(const Ctx& ctx, const char* ws, size_t rec_bytes,
                                int32_t* counts, cudaStream_t s);
 cudaError_t launch_slot_swaps(const Ctx& ctx, uint8_t* pool, size_t stride, size_t record_bytes, int32_t* slot_of,
                               int n_slots, const SwapBatch& batch, int n, cudaStream_t s);
+
+// balance.cu: the router's balance loss and the gradient of its logits
+size_t balance_ws_bytes(int E);
+cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
+                           const uint8_t* mask, int T, float* stats, int32_t* counts, float* prob, void* ws,
+                           cudaStream_t s);
+cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
+                                    const float* gate, const uint8_t* mask, int T, const float* stats,
+                                    const int32_t* counts, const float* d_loss, const float* d_gate, float* d_logits,
+                                    cudaStream_t s);
+cudaError_t balance_init(const Ctx& ctx);
+
+// mx4_quant.cu: rows to 4-bit MX codes and scales, and back
+__host__ __device__ __forceinline__ int mx4_pitch(int cols) { return (cols / kBlock + 15) / 16 * 16; }
+cudaError_t launch_mx4_quantize(const void* x, int type, int rows, int cols, size_t ld, uint8_t* codes,
+                                uint8_t* scales, cudaStream_t s);
+cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int cols, void* out, int type,
+                                  size_t ld, cudaStream_t s);
+
+// mx4_product.cu: the (grouped) product of two MX matrices
+struct Mx4Args {
+  const uint8_t *x_codes, *x_scales;
+  int x_rows;
+  moe_mx4_matrix w;
+  const moe_grouping* g;  // or null: one group, slot 0
+  int shared_slot;        // slot of the group of rows n_pairs .. n_pairs + T - 1, or -1
+  bool gather, swiglu, gate;
+  void* out;
+  int out_type;
+  size_t ld;
+};
+cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s);
+cudaError_t mx4_product_init(const Ctx& ctx);
 
 // kernel attribute set-up, once per context
 cudaError_t decode_init(Ctx& ctx);

@@ -77,6 +77,17 @@ class LayerCfg:
 TINY = LayerCfg(d=256, f=128, E=16, k=2)
 FULL = LayerCfg(d=2048, f=768, E=512, k=10)
 
+TYPE_BF16, TYPE_FP16, TYPE_FP32 = range(3)  # element types of the MX calls
+MX4_GATHER, MX4_SWIGLU, MX4_GATE = 1, 2, 4
+MX4_BLOCK = 32  # values per scale
+
+
+class _Mx4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("code_stride", ctypes.c_size_t),
+                ("scale_stride", ctypes.c_size_t), ("n_slots", ctypes.c_int), ("rows", ctypes.c_int),
+                ("cols", ctypes.c_int)]
+
+
 _P, _I, _Z, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
 _SIGS = {
     "moe_ctx_create": (_I, [_I, ctypes.POINTER(ctypes.c_void_p)]),
@@ -106,6 +117,14 @@ _SIGS = {
     "moe_layer_forward_static": (_I, [_P, ctypes.POINTER(_Cfg), _P, _I, _P, _P, _P, _I, _P, _Z, _P, _P, _S]),
     "moe_usage_count": (_I, [_P, ctypes.POINTER(_Cfg), _I, _I, _P, _Z, _P, _S]),
     "moe_slot_swap": (_I, [_P, ctypes.POINTER(_Cfg), _P, _Z, _P, _I, _I, _P, _P, _I, _S]),
+    "moe_balance_workspace_bytes": (_Z, [ctypes.POINTER(_Cfg)]),
+    "moe_balance_loss": (_I, [_P, ctypes.POINTER(_Cfg), _P, _P, _P, _I, _P, _P, _P, _P, _Z, _S]),
+    "moe_balance_loss_backward": (_I, [_P, ctypes.POINTER(_Cfg), _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _S]),
+    "moe_mx4_scale_pitch": (_Z, [_I]),
+    "moe_mx4_quantize": (_I, [_P, _P, _I, _I, _I, _Z, _P, _P, _S]),
+    "moe_mx4_dequantize": (_I, [_P, _P, _P, _I, _I, _P, _I, _Z, _S]),
+    "moe_mx4_product": (_I, [_P, _P, _P, _I, ctypes.POINTER(_Mx4), ctypes.POINTER(Grouping), _I, _I, _P, _I, _Z,
+                             _S]),
 }
 
 _lib = None
@@ -268,6 +287,75 @@ class Context:
         do the two table entries (a, b: host index arrays into the flat device table slot_of)."""
         _check(self.slot_swap_status(cfg, pool, stride, slot_of, n_slots, a, b, stream), "moe_slot_swap")
 
+    # -- the router's balance loss -------------------------------------------------
+    def balance_loss_status(self, cfg, logits, idx, mask, T, stats, counts, prob, ws, stream=None) -> int:
+        return self.lib.moe_balance_loss(self.h, ctypes.byref(cfg.c()), _ptr(logits), _ptr(idx), _ptr(mask), T,
+                                         _ptr(stats), _ptr(counts), _ptr(prob), _ptr(ws),
+                                         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+
+    def balance_loss(self, cfg, logits, idx, mask, T, stats, counts, prob, ws, stream=None) -> None:
+        """moe_balance_loss: stats [4] fp32 (balance loss, z loss, tokens that count, largest load), counts [E]
+        int32 and prob [E] fp32 from logits [T, E] fp32, idx [T, k] int32 and mask [T] uint8 or None."""
+        _check(self.balance_loss_status(cfg, logits, idx, mask, T, stats, counts, prob, ws, stream),
+               "moe_balance_loss")
+
+    def balance_loss_backward_status(self, cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate, d_logits,
+                                     stream=None) -> int:
+        return self.lib.moe_balance_loss_backward(self.h, ctypes.byref(cfg.c()), _ptr(logits), _ptr(idx), _ptr(gate),
+                                                  _ptr(mask), T, _ptr(stats), _ptr(counts), _ptr(d_loss),
+                                                  _ptr(d_gate), _ptr(d_logits), _stream(stream))
+
+    def balance_loss_backward(self, cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate, d_logits,
+                              stream=None) -> None:
+        """moe_balance_loss_backward: d_logits [T, E] of d_loss[0] * stats[0] + d_loss[1] * stats[1] and, unless
+        d_gate is None, of the gates [T, k]."""
+        _check(self.balance_loss_backward_status(cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate,
+                                                 d_logits, stream), "moe_balance_loss_backward")
+
+    # -- 4-bit experts in the MX format ----------------------------------------------
+    def mx4_quantize_status(self, x, codes, scales, stream=None) -> int:
+        rows, cols, ld = _rows(x)
+        if _bad_mx4(codes, scales, rows, cols):
+            return EINVAL
+        return self.lib.moe_mx4_quantize(self.h, _ptr(x), _type(x), rows, cols, ld, _ptr(codes), _ptr(scales),
+                                         _stream(stream))
+
+    def mx4_quantize(self, x, codes, scales, stream=None) -> None:
+        """moe_mx4_quantize: x [rows, cols] (bf16, fp16 or fp32, any row stride) to codes and scales as
+        mx4_buffers gives them."""
+        _check(self.mx4_quantize_status(x, codes, scales, stream), "moe_mx4_quantize")
+
+    def mx4_dequantize_status(self, codes, scales, out, stream=None) -> int:
+        rows, cols, ld = _rows(out)
+        if _bad_mx4(codes, scales, rows, cols):
+            return EINVAL
+        return self.lib.moe_mx4_dequantize(self.h, _ptr(codes), _ptr(scales), rows, cols, _ptr(out), _type(out), ld,
+                                           _stream(stream))
+
+    def mx4_dequantize(self, codes, scales, out, stream=None) -> None:
+        """moe_mx4_dequantize: the values of codes and scales to out [rows, cols] (bf16, fp16 or fp32)."""
+        _check(self.mx4_dequantize_status(codes, scales, out, stream), "moe_mx4_dequantize")
+
+    def mx4_product_status(self, codes, scales, w: "Mx4Matrix", out, grouping=None, shared_slot=-1, gather=False,
+                           swiglu=False, gate=False, stream=None) -> int:
+        rows, cols, ld = _rows(out)
+        x_rows = codes.shape[0]
+        if _bad_mx4(codes, scales, x_rows, w.cols) or cols != (w.rows // 2 if swiglu else w.rows):
+            return EINVAL
+        need = x_rows if grouping is None else grouping.n_pairs + (grouping.T if shared_slot >= 0 else 0)
+        if rows < need:
+            return EINVAL
+        flags = (MX4_GATHER if gather else 0) | (MX4_SWIGLU if swiglu else 0) | (MX4_GATE if gate else 0)
+        return self.lib.moe_mx4_product(self.h, _ptr(codes), _ptr(scales), x_rows, ctypes.byref(w.c()),
+                                        None if grouping is None else ctypes.byref(grouping), shared_slot, flags,
+                                        _ptr(out), _type(out), ld, _stream(stream))
+
+    def mx4_product(self, codes, scales, w: "Mx4Matrix", out, grouping=None, shared_slot=-1, gather=False,
+                    swiglu=False, gate=False, stream=None) -> None:
+        """moe_mx4_product: out = x w^T of 4-bit rows (codes, scales) and the matrices w, one matrix or grouped."""
+        _check(self.mx4_product_status(codes, scales, w, out, grouping, shared_slot, gather, swiglu, gate, stream),
+               "moe_mx4_product")
+
     def layer_routing(self, cfg, T, ws, stack_layers=None, layer=0) -> dict:
         """The routing a whole-step call with workspace `ws` computed (moe_layer_routing; with
         stack_layers=L, layer `layer` of a moe_stack_forward workspace), as torch views into ws:
@@ -373,7 +461,73 @@ class PreparedStack:
         _check(self.status(x, bias, y), "moe_stack_forward")
 
 
+# ------------------------------------------------------------------ 4-bit MX matrices
+
+def _rows(t):
+    """(rows, cols, elements from row to row) of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise MoeError(EINVAL, f"a 2-D tensor with contiguous rows is needed, got {tuple(t.shape)}, {t.stride()}")
+    return t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _type(t) -> int:
+    import torch
+    return {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}.get(t.dtype, -1)
+
+
+def _bad_mx4(codes, scales, rows, cols) -> bool:
+    """Whether codes and scales are not the contiguous bytes of [rows, cols] MX rows."""
+    pitch = mx4_scale_pitch(cols)
+    return any(t.element_size() != 1 or not t.is_contiguous() or tuple(t.shape) != (rows, n)
+               for t, n in ((codes, cols // 2), (scales, pitch))) if pitch else False
+
+
+def mx4_scale_pitch(cols: int) -> int:
+    """Bytes from one row of scales to the next; 0 where cols is no multiple of 32 or too large."""
+    return int(load_library().moe_mx4_scale_pitch(cols))
+
+
+def mx4_buffers(rows: int, cols: int, device="cuda"):
+    """Uninitialised codes [rows, cols/2] and scales [rows, pitch] (uint8) of an MX matrix."""
+    import torch
+    pitch = mx4_scale_pitch(cols)
+    if pitch == 0 or rows < 0:
+        raise MoeError(EINVAL if rows < 0 or cols <= 0 else EUNSUPPORTED, "moe_mx4_scale_pitch")
+    return (torch.empty(rows, cols // 2, dtype=torch.uint8, device=device),
+            torch.empty(rows, pitch, dtype=torch.uint8, device=device))
+
+
+class Mx4Matrix:
+    """One matrix or a pool of them in MX form: codes [rows, cols/2] or [slots, rows, cols/2] and scales
+    [rows, pitch] or [slots, rows, pitch] (uint8; each matrix contiguous, the slots at any 16-byte stride)."""
+
+    def __init__(self, codes, scales, cols: int):
+        if codes.dim() == 2:
+            codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
+        pitch = mx4_scale_pitch(cols)
+        if pitch == 0 or codes.dim() != 3 or scales.dim() != 3:
+            raise MoeError(EINVAL, "Mx4Matrix")
+        self.n_slots, self.rows, self.cols = codes.shape[0], codes.shape[1], cols
+        for t, n in ((codes, cols // 2), (scales, pitch)):
+            if t.element_size() != 1 or tuple(t.shape) != (self.n_slots, self.rows, n) or not t[0].is_contiguous():
+                raise MoeError(EINVAL, f"Mx4Matrix: a part of shape {tuple(t.shape)} for {cols} columns")
+        self.codes, self.scales = codes, scales
+        self._c = _Mx4(codes.data_ptr(), scales.data_ptr(), codes.stride(0), scales.stride(0), self.n_slots, self.rows,
+                       cols)
+
+    def c(self) -> _Mx4:
+        return self._c
+
+
 # ------------------------------------------------------------------ buffers
+
+def balance_workspace(cfg: LayerCfg, device="cuda"):
+    import torch
+    n = int(load_library().moe_balance_workspace_bytes(ctypes.byref(cfg.c())))
+    if n == 0:
+        raise MoeError(EINVAL, "moe_balance_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
 
 def workspace(cfg: LayerCfg, T: int, device="cuda"):
     import torch

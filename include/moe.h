@@ -383,6 +383,113 @@ MOE_API moe_status moe_layer_forward_static(moe_ctx* ctx, const moe_layer_cfg* c
                                     size_t slot_stride, const uint8_t* shared_expert, void* y,
                                     moe_stream stream);
 
+/* ---- the router's balance loss -------------------------------------------- */
+
+/* What a router is trained with beside the model's own loss: how many choices
+ * each expert got, a loss that evens them out, and the gradient of the logits.
+ *
+ * moe_balance_loss: a token counts when mask is NULL or mask[t] != 0, and at
+ * least one of its E logits is above -infinity (a row of -infinity may use no
+ * expert). Over the n tokens that count, with p_t = softmax(logits[t]),
+ *   counts[e] = number of (t, j) with idx[t, j] = e              (exact)
+ *   prob[e]   = sum_t p_t[e] / n
+ *   stats[0]  = E / (k n) * sum_e counts[e] * prob[e]   (1 for an even router)
+ *   stats[1]  = sum_t (log sum_e exp logits[t, e])^2 / n         (the z loss)
+ *   stats[2]  = n
+ *   stats[3]  = E / (k n) * max_e counts[e]             (1 for an even router)
+ * and all of them 0 where n = 0 (T = 0 among them). logits [T, E] fp32 and
+ * idx [T, k] int32 as moe_router_topk gives them (the bias included); mask
+ * [T] bytes or NULL; stats [4], prob [E] fp32, counts [E] int32 out. Sums over
+ * tokens are taken in a fixed order: equal calls give equal bits. An idx
+ * outside [0, E) counts nowhere and is reported as MOE_EDEVICE. ws:
+ * moe_balance_workspace_bytes(cfg), 256-byte aligned, scratch of this call.
+ *
+ * moe_balance_loss_backward: d_logits [T, E] = the gradient of
+ *   d_loss[0] * stats[0] + d_loss[1] * stats[1] + sum d_gate * gate
+ * by the logits; counts are whole numbers and take no gradient. d_loss: [2]
+ * fp32 on the device; gate [T, k] as moe_topk gave it under cfg->renorm;
+ * d_gate: [T, k], or NULL for the losses alone (gate may then be NULL);
+ * stats, counts: from moe_balance_loss on the same logits, idx and mask. Rows
+ * that do not count get 0, their gates' part included. An expert that a row
+ * names twice takes both parts; an idx outside [0, E) none. d_logits must not
+ * overlap the inputs. */
+MOE_API size_t moe_balance_workspace_bytes(const moe_layer_cfg* cfg);
+MOE_API moe_status moe_balance_loss(moe_ctx* ctx, const moe_layer_cfg* cfg, const float* logits, const int32_t* idx,
+                                    const uint8_t* mask, int T, float* stats, int32_t* counts, float* prob, void* ws,
+                                    size_t ws_bytes, moe_stream stream);
+MOE_API moe_status moe_balance_loss_backward(moe_ctx* ctx, const moe_layer_cfg* cfg, const float* logits,
+                                             const int32_t* idx, const float* gate, const uint8_t* mask, int T,
+                                             const float* stats, const int32_t* counts, const float* d_loss,
+                                             const float* d_gate, float* d_logits, moe_stream stream);
+
+/* ---- 4-bit experts in the MX format ---------------------------------------- */
+
+/* Microscaled 4-bit floating point (OCP MX, element E2M1, scale E8M0): a row
+ * is cut into blocks of 32 values with one scale 2^(s - 127) each, s a byte
+ * (255: NaN), and a value is its code's level times the scale. Code bits: sign,
+ * then the levels 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   codes   [rows, cols/2]: value c of a row in byte c/2, the even one in the
+ *           low four bits; rows follow each other without a gap.
+ *   scales  [rows, moe_mx4_scale_pitch(cols)]: block b of a row in byte b; the
+ *           pitch is cols/32 rounded up to 16, the bytes past cols/32 are
+ *           written as 0 and never read as scales.
+ * cols: a multiple of 32, at most 65536. Both arrays 16-byte aligned. */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_FP16 1
+#define MOE_TYPE_FP32 2
+
+/* Bytes from one row of scales to the next (0 if cols is invalid). */
+MOE_API size_t moe_mx4_scale_pitch(int cols);
+
+/* x [rows, cols] of x_type with ld elements from row to row (ld >= cols), to
+ * codes and scales: per block, s - 127 = clamp(floor(log2 max|x|) - 2, -127,
+ * 127), values over the scale rounded to the nearest level (ties to the code
+ * with an even last bit, magnitudes above 6 to 6). A block of zeros gets s = 0;
+ * a block that holds a NaN or an infinity gets s = 255 and codes 0. rows = 0 is
+ * a no-op. */
+MOE_API moe_status moe_mx4_quantize(moe_ctx* ctx, const void* x, int x_type, int rows, int cols, size_t ld,
+                                    uint8_t* codes, uint8_t* scales, moe_stream stream);
+
+/* The values that codes and scales stand for, rounded once to out_type (exact
+ * in fp32 but for 2^128 and above, which become infinite, and in bf16 where
+ * the value is normal). out [rows, cols], ld elements from row to row. */
+MOE_API moe_status moe_mx4_dequantize(moe_ctx* ctx, const uint8_t* codes, const uint8_t* scales, int rows, int cols,
+                                      void* out, int out_type, size_t ld, moe_stream stream);
+
+/* n_slots matrices [rows, cols] in MX form: slot s at codes + s * code_stride
+ * and scales + s * scale_stride (bytes, multiples of 16, at least the
+ * matrix's own size; not looked at when n_slots = 1). rows: a multiple of 16. */
+typedef struct {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  size_t code_stride, scale_stride;
+  int n_slots, rows, cols;
+} moe_mx4_matrix;
+
+#define MOE_MX4_GATHER 1 /* x holds one row per token, not per output row */
+#define MOE_MX4_SWIGLU 2 /* w's rows 2c, 2c+1 are gate and up row of channel c: out = silu(gate) * up */
+#define MOE_MX4_GATE   4 /* output rows of pairs are multiplied by pair_gate */
+
+/* out = x w^T on 4-bit codes, sums in fp32, rounded once to out_type.
+ *   grouping == NULL: out row r = x row r times w's only matrix (slot 0),
+ *     r < x_rows; shared_slot must be -1 and MOE_MX4_GATHER, _GATE unset.
+ *   grouping != NULL (from moe_group_tokens): out row p of sorted pair p is
+ *     the pair's x row times the matrix in the pair's slot; with shared_slot
+ *     >= 0 the rows n_pairs + t follow, token t times that slot's matrix. The x
+ *     row is pair_token[p] (or t) with MOE_MX4_GATHER (x_rows = T), else the
+ *     output row's own number (x_rows >= the output rows). Rows of pairs that
+ *     the grouping left out (MOE_SLOT_ABSENT) are left as they were.
+ * out: [.., w->rows], or w->rows / 2 columns with MOE_MX4_SWIGLU; ld elements
+ * from row to row; aligned to its element. With _GATHER | _SWIGLU this is the
+ * gate/up half of an expert FFN on 4-bit weights, and with _GATE into fp32
+ * rows its down half, which moe_combine joins, as moe_expert_ffn_q2 with
+ * z_rows does for 2-bit records. A slot >= w->n_slots or a pair_token outside
+ * x is reported as MOE_EDEVICE; its rows are not written (a bad token's row
+ * counts as zeros). */
+MOE_API moe_status moe_mx4_product(moe_ctx* ctx, const uint8_t* x_codes, const uint8_t* x_scales, int x_rows,
+                                   const moe_mx4_matrix* w, const moe_grouping* grouping, int shared_slot, int flags,
+                                   void* out, int out_type, size_t ld, moe_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
