@@ -148,6 +148,8 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
   const int E = R.E, k = R.k;
   for (int e = threadIdx.x; e < E; e += kBThreads) hist[e] = 0;
+  grid_dep_launch();  // the next kernel of the stream sets up meanwhile
+  grid_dep_wait();
   __syncthreads();
 
   float acc[SLOTS * 4];
@@ -293,6 +295,7 @@ __global__ void __launch_bounds__(kBThreads)
   constexpr int kRows = 32 / LANES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
   const int E = R.E, k = R.k;
+  grid_dep_wait();
   const float n = fmaxf(__ldg(stats + 2), 1.f);
   const float ca = __ldg(d_loss) * (static_cast<float>(E) / k) / n / n;
   const float cz = __ldg(d_loss + 1) * 2.f / n;
@@ -422,20 +425,11 @@ cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* 
   P.tok = P.cnt + static_cast<size_t>(kBalanceMaxCtas) * E;
   const bool vec = rows_vec(logits, E);
   const cudaError_t e = by_experts(E, [&](auto lanes, auto slots) {
-    balance_rows_kernel<lanes.value, slots.value><<<n, kBThreads, kBWarps * E * 4, s>>>(R, P, O, vec);
-    return cudaGetLastError();
+    return launch_dependent(balance_rows_kernel<lanes.value, slots.value>, n, kBThreads,
+                            static_cast<size_t>(kBWarps) * E * 4, s, R, P, O, vec);
   });
   if (e != cudaSuccess || n == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kFinCtas);
-  cfg.blockDim = dim3(kBThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, balance_finish_kernel, P, O, n, E, c.k);
+  return launch_dependent(balance_finish_kernel, kFinCtas, kBThreads, 0, s, P, O, n, E, c.k);
 }
 
 cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
@@ -449,9 +443,8 @@ cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, cons
   const int want = (T + per_cta - 1) / per_cta;
   const int n = want < 2 * ctx.num_sms ? want : 2 * ctx.num_sms;
   return by_experts(E, [&](auto lanes, auto slots) {
-    balance_backward_kernel<lanes.value, slots.value><<<n, kBThreads, 0, s>>>(R, stats, counts, d_loss, d_gate,
-                                                                            c.renorm != 0, vec, d_logits);
-    return cudaGetLastError();
+    return launch_dependent(balance_backward_kernel<lanes.value, slots.value>, n, kBThreads, 0, s, R, stats, counts,
+                            d_loss, d_gate, c.renorm != 0, vec, d_logits);
   });
 }
 

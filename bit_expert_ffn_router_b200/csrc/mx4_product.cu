@@ -36,7 +36,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 576;
 constexpr int kBM = 128;                      // weight rows per tile
 constexpr int kBN = 208;                      // x rows per tile, at most
 constexpr int kBK = 256;                      // K values per stage: 128 bytes of codes per row
@@ -46,6 +46,11 @@ constexpr int kAcc = kBN;                     // TMEM columns of one accumulator
 constexpr int kSfCols = 24;                   // TMEM columns of a stage's scales: w 2 x 4, x 2 x 8
 static_assert(2 * kAcc + kStages * kSfCols <= 512, "tensor memory budget");
 constexpr int kScaleThreads = 128;
+constexpr int kEpiThreads = 256;
+constexpr int kGatherThreads = 128;
+constexpr int kGatherRows = kBN / (kGatherThreads / 8);  // rows of a stage per gather thread
+constexpr int kGatherLag = 2;                            // stages between issuing a copy and announcing it
+constexpr int kBoxA = 64, kBoxB = 16;                    // x rows of the two TMA boxes
 
 struct Smem {
   static constexpr int kA = 0;                          // kBM rows x 128 bytes, 128B-swizzled
@@ -60,10 +65,11 @@ static_assert(Smem::kStage % 1024 == 0, "swizzle atoms start on 1024 bytes");
 // The groups' row tiles, laid end to end: group i's first is prefix[i].
 struct Table {
   uint64_t full[kStages];      // TMA (tx): codes landed
+  uint64_t x_full[kStages];    // gather threads (count 128): x rows landed, where tokens name them
   uint64_t sf_full[kStages];   // scale threads (count 128)
   uint64_t empty[kStages];     // MMA commit: codes and scales read
   uint64_t d_full[2];          // MMA commit: accumulator complete
-  uint64_t d_empty[2];         // epilogue (count 128)
+  uint64_t d_empty[2];         // epilogue (count 256)
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
@@ -78,7 +84,7 @@ constexpr int kSmemBytes = Smem::kTable + static_cast<int>(sizeof(Table)) + 1024
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
 struct Params {
-  const uint8_t *xs, *ws;  // scales
+  const uint8_t *xc, *xs, *ws;  // x codes; scales
   size_t ws_stride;
   int x_rows, w_rows, n_slots, K, pitch, m_tiles;
   bool grouped;
@@ -199,13 +205,10 @@ __device__ __forceinline__ int source_row(const Params& P, int p) {
   return min(max(t, 0), P.x_rows - 1);
 }
 
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int c0, int r0, int r1, int r2, int r3,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-      "%5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
-      : "memory");
+// 16 bytes to shared memory without passing through registers; zeros where
+// `live` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
 // 32 rows of 16 bytes, to four 32-bit columns of every lane quarter.
@@ -281,47 +284,61 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 // 16 accumulator columns (output rows p0 .. p0 + 15, `left` of them real) of
-// weight row wr in v.
+// weight row wr in v; lane i holds the gate of row p0 + i % 16.
 template <typename T, bool SWIGLU>
-__device__ __forceinline__ void store16(const Params& P, const float* v, int wr, long long p0, int left, float gate_l,
-                                        int gate_lane0) {
-  T* out = static_cast<T*>(P.out);
-  const bool odd = (threadIdx.x & 1) != 0, live = wr < P.w_rows;
+__device__ __forceinline__ void store16(const Params& P, const float* v, int wr, long long p0, int left, float gate_l) {
+  const bool live = wr < P.w_rows;
+  T* out = static_cast<T*>(P.out) + p0 * P.ld;
   if constexpr (!SWIGLU && sizeof(T) == 4) {
+    float o[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float g = P.gate ? __shfl_sync(0xffffffffu, gate_l, gate_lane0 + i) : 1.f;
-      if (live && i < left) out[(p0 + i) * P.ld + wr] = narrow<T>(v[i] * g);
-    }
+    for (int i = 0; i < 16; ++i) o[i] = P.gate ? v[i] * __shfl_sync(0xffffffffu, gate_l, i) : v[i];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (live && i < left) out[i * P.ld + wr] = narrow<T>(o[i]);
   } else {
     // Neighbouring lanes hold rows 2c and 2c + 1 of w; of every two columns the
     // even lane takes the first with both rows, the odd lane the second.
+    const int odd = threadIdx.x & 1;
+    float a[8], b[8];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-      float a = odd ? other : v[i], b = odd ? v[i + 1] : other;
-      const int col = i + (odd ? 1 : 0);
-      const float g = P.gate ? __shfl_sync(0xffffffffu, gate_l, gate_lane0 + col) : 1.f;
-      if (!live || col >= left) continue;
-      T* row = out + (p0 + col) * P.ld;
-      if (SWIGLU) {
-        row[wr >> 1] = narrow<T>(__fdividef(a, 1.f + __expf(-a)) * b * g);
-      } else {
-        a *= g, b *= g;
-        if (P.pack) {
-          *reinterpret_cast<uint32_t*>(row + (wr & ~1)) = pack2<T>(a, b);
-        } else {
-          row[wr & ~1] = narrow<T>(a);
-          row[wr | 1] = narrow<T>(b);
-        }
+    for (int i = 0; i < 8; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+      a[i] = odd ? other : v[2 * i];
+      b[i] = odd ? v[2 * i + 1] : other;
+      // h is rounded to 16 bits or summed in fp32 far above these errors: the
+      // fast exponential and division (2 + 1.2 |a| steps, 2 steps)
+      if (SWIGLU) a[i] = __fdividef(a[i], 1.f + __expf(-a[i])) * b[i];
+      if (P.gate) {
+        const float g = __shfl_sync(0xffffffffu, gate_l, 2 * i + odd);
+        a[i] *= g, b[i] *= g;
       }
+    }
+    out += odd * P.ld + (SWIGLU ? wr >> 1 : wr & ~1);
+    left -= odd;
+    if (SWIGLU) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (live && 2 * i < left) out[2 * i * P.ld] = narrow<T>(a[i]);
+    } else if (P.pack) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (live && 2 * i < left) *reinterpret_cast<uint32_t*>(out + 2 * i * P.ld) = pack2<T>(a[i], b[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (live && 2 * i < left) {
+          out[2 * i * P.ld] = narrow<T>(a[i]);
+          out[2 * i * P.ld + 1] = narrow<T>(b[i]);
+        }
     }
   }
 }
 
 template <typename T, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
-    mx4_product_kernel(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX, const Params P) {
+    mx4_product_kernel(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tXa,
+                       const __grid_constant__ CUtensorMap tXb, const Params P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Table* B = reinterpret_cast<Table*>(smem + Smem::kTable);
@@ -330,12 +347,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&B->full[i], 1);
+      mbar_init(&B->x_full[i], kGatherThreads);
       mbar_init(&B->sf_full[i], kScaleThreads);
       mbar_init(&B->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->d_full[i], 1);
-      mbar_init(&B->d_empty[i], 128);
+      mbar_init(&B->d_empty[i], kEpiThreads);
     }
     mbar_init(&B->mma_done, 1);
     B->abort_flag = 0;
@@ -355,37 +373,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------------- codes
     int g = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; w < total && ok; w += G) {
-      const Item it = item_at(P, *B, w);
-      const int quads = it.n16 / 4;  // gathers per stage: lane i takes quads i and i + 32
-      int src[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 4 * (lane + 32 * h) + i;
-          src[h][i] = source_row(P, it.row0 + min(r, it.rows - 1));
-        }
-      const uint32_t tx = static_cast<uint32_t>(kBM + it.n16) * 128u;
-      for (int k = 0; k < n_k; ++k, ++g) {
-        const int st = g % kStages;
-        if (g >= kStages && !wait_warp(B, &B->empty[st], ((g / kStages) - 1) & 1, P, 1)) {
-          ok = false;
-          break;
-        }
-        uint8_t* stage = smem + st * Smem::kStage;
-        if (lane == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int w = blockIdx.x; w < total && ok; w += G) {
+        const Item it = item_at(P, *B, w);
+        const uint32_t tx = static_cast<uint32_t>(kBM + (P.gather ? 0 : it.n16)) * 128u;
+        for (int k = 0; k < n_k; ++k, ++g) {
+          const int st = g % kStages;
+          if (g >= kStages && !wait_bar(B, &B->empty[st], ((g / kStages) - 1) & 1, P, 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* stage = smem + st * Smem::kStage;
           mbar_arrive_expect_tx(&B->full[st], tx);
           tma_load_3d(stage + Smem::kA, &tW, k * (kBK / 2), it.m * kBM, it.slot, &B->full[st]);
+          if (P.gather) continue;
+          int r = 0;  // n16 rows: boxes of 64, the rest in boxes of 16
+          for (; r + kBoxA <= it.n16; r += kBoxA)
+            tma_load_2d(stage + Smem::kB + r * 128, &tXa, k * (kBK / 2), it.row0 + r, &B->full[st]);
+          for (; r < it.n16; r += kBoxB)
+            tma_load_2d(stage + Smem::kB + r * 128, &tXb, k * (kBK / 2), it.row0 + r, &B->full[st]);
         }
-        __syncwarp();
-        if (lane < quads)
-          tma_gather4(stage + Smem::kB + lane * 512, &tX, k * (kBK / 2), src[0][0], src[0][1], src[0][2], src[0][3],
-                      &B->full[st]);
-        if (lane + 32 < quads)
-          tma_gather4(stage + Smem::kB + (lane + 32) * 512, &tX, k * (kBK / 2), src[1][0], src[1][1], src[1][2],
-                      src[1][3], &B->full[st]);
       }
     }
     // every copy this warp issued lands before the CTA may exit (bounded wait)
@@ -408,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < n_k; ++k, ++g) {
           const int st = g % kStages;
           const uint32_t ph = (g / kStages) & 1;
-          if (!wait_bar(B, &B->full[st], ph, P, 3) || !wait_bar(B, &B->sf_full[st], ph, P, 4)) {
+          if (!wait_bar(B, &B->full[st], ph, P, 3) || !wait_bar(B, &B->sf_full[st], ph, P, 4) ||
+              (P.gather && !wait_bar(B, &B->x_full[st], ph, P, 7))) {
             ok = false;
             break;
           }
@@ -490,9 +499,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (warp >= 14) {
+    // ---------------------------------------------------------- gathered x rows
+    // Thread i copies 16-byte chunk i % 8 of rows i / 8, i / 8 + 16, ... of a
+    // stage to its swizzled place (chunk ^ row % 8).
+    if (P.gather) {
+      const int c = threadIdx.x & 7, r0 = (threadIdx.x - 448) >> 3;
+      const uint32_t dst0 = smem_u32(smem + Smem::kB) + static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
+      const int row_b = P.K / 2;
+      int g = 0, told = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; w < total && ok; w += G) {
+        const Item it = item_at(P, *B, w);
+        int src[kGatherRows];
+#pragma unroll
+        for (int j = 0; j < kGatherRows; ++j) {
+          const int r = r0 + 16 * j;
+          src[j] = r < it.n16 ? source_row(P, it.row0 + min(r, it.rows - 1)) : 0;
+        }
+        for (int k = 0; k < n_k; ++k, ++g) {
+          const int st = g % kStages;
+          if (g >= kStages && !wait_warp(B, &B->empty[st], ((g / kStages) - 1) & 1, P, 8)) {
+            ok = false;
+            break;
+          }
+          const int col = k * (kBK / 2) + c * 16;
+          const bool live = col < row_b;
+          const uint8_t* base = P.xc + (live ? col : 0);
+          const uint32_t dst = dst0 + static_cast<uint32_t>(st * Smem::kStage);
+#pragma unroll
+          for (int j = 0; j < kGatherRows; ++j)
+            if (r0 + 16 * j < it.n16)
+              copy16(dst + j * 16 * 128, base + static_cast<size_t>(src[j]) * row_b, live);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (g - told >= kGatherLag) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kGatherLag) : "memory");
+            fence_async_smem();
+            mbar_arrive(&B->x_full[told % kStages]);
+            ++told;
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      for (; told < g; ++told) mbar_arrive(&B->x_full[told % kStages]);
+    }
   } else {
     // ---------------------------------------------------------- epilogue
-    const int q = warp & 3;  // TMEM lane quarter of this warp
+    const int q = warp & 3;           // TMEM lane quarter of this warp
+    const int half = (warp - 6) >> 2;  // takes the 16-column chunks of this parity
     int i = 0;
     for (int w = blockIdx.x; w < total; w += G, ++i) {
       const Item it = item_at(P, *B, w);
@@ -501,16 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t base = tmem + static_cast<uint32_t>(acc * kAcc) + (static_cast<uint32_t>(q * 32) << 16);
       const int wr = it.m * kBM + q * 32 + lane;
-      float gate_l = 1.f;
-      for (int c0 = 0; c0 < it.rows; c0 += 16) {
-        if (P.gate && (c0 & 31) == 0) {  // lane i takes the gate of row c0 + i
-          const int p = it.row0 + c0 + lane;
-          gate_l = c0 + lane < it.rows && p < P.n_pairs ? __ldg(P.pair_gate + p) : 1.f;
+      for (int c0 = 16 * half; c0 < it.rows; c0 += 32) {
+        float gate_l = 1.f;
+        if (P.gate) {
+          const int c = c0 + (lane & 15), p = it.row0 + c;
+          if (c < it.rows && p < P.n_pairs) gate_l = __ldg(P.pair_gate + p);
         }
         __syncwarp();
         float v[16];
         tmem_ld16(base + c0, v);
-        store16<T, SWIGLU>(P, v, wr, static_cast<long long>(it.row0) + c0, it.rows - c0, gate_l, c0 & 16);
+        store16<T, SWIGLU>(P, v, wr, static_cast<long long>(it.row0) + c0, it.rows - c0, gate_l);
       }
       tc_fence_before();
       mbar_arrive(&B->d_empty[acc]);
@@ -579,6 +634,7 @@ cudaError_t mx4_product_init(const Ctx& ctx) {
 cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s) {
   if (encoder() == nullptr) return cudaErrorNotSupported;
   Params P{};
+  P.xc = a.x_codes;
   P.xs = a.x_scales;
   P.ws = a.w.scales;
   P.ws_stride = a.w.n_slots > 1 ? a.w.scale_stride : 0;
@@ -614,10 +670,13 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   if (items > 0x7fffffff) return cudaErrorNotSupported;
 
   const int row_b = a.w.cols / 2;
-  CUtensorMap tw, tx;
+  CUtensorMap tw, txa, txb;
   const size_t stride = a.w.n_slots > 1 ? a.w.code_stride : static_cast<size_t>(a.w.rows) * row_b;
-  if (!map_codes(&tw, a.w.codes, row_b, a.w.rows, a.w.n_slots, stride, 3, kBM) ||
-      !map_codes(&tx, a.x_codes, row_b, a.x_rows, 1, 0, 2, 1))
+  if (!map_codes(&tw, a.w.codes, row_b, a.w.rows, a.w.n_slots, stride, 3, kBM)) return cudaErrorInvalidValue;
+  if (a.gather)
+    txa = txb = tw;  // not used: the x rows are copied one by one
+  else if (!map_codes(&txa, a.x_codes, row_b, a.x_rows, 1, 0, 2, kBoxA) ||
+           !map_codes(&txb, a.x_codes, row_b, a.x_rows, 1, 0, 2, kBoxB))
     return cudaErrorInvalidValue;
 
   cudaLaunchConfig_t cfg = {};
@@ -630,7 +689,7 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void* args[] = {&tw, &tx, &P};
+  void* args[] = {&tw, &txa, &txb, &P};
   return cudaLaunchKernelExC(&cfg, kernel_of(a.out_type, a.swiglu), args);
 }
 

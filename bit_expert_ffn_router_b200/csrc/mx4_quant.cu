@@ -18,6 +18,7 @@
 // fp32), a block's maximum takes two shuffles among its four lanes, the codes
 // leave as one 4-byte word per thread.
 #include "moe_internal.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -122,6 +123,8 @@ __global__ void __launch_bounds__(kQThreads) mx4_quantize_kernel(const T* __rest
                                                                  uint8_t* __restrict__ scales) {
   const long long u0 = static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits);
   const RowOf rows(u0, upr, magic);
+  grid_dep_launch();  // a product that follows sets up meanwhile; it waits for this grid's end
+  grid_dep_wait();
   float v[kQUnits][8];
   long long row[kQUnits];
   uint32_t unit[kQUnits];
@@ -178,6 +181,8 @@ __global__ void __launch_bounds__(kQThreads) mx4_dequantize_kernel(const uint8_t
                                                                    int pitch, T* __restrict__ out, long long ld) {
   const long long u0 = static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits);
   const RowOf rows(u0, upr, magic);
+  grid_dep_launch();  // a product that follows sets up meanwhile; it waits for this grid's end
+  grid_dep_wait();
   uint32_t c[kQUnits], s[kQUnits];
   long long row[kQUnits];
   uint32_t unit[kQUnits];
@@ -237,10 +242,10 @@ cudaError_t quantize(const void* x, int rows, int cols, size_t ld, uint8_t* code
   const T* p = static_cast<const T*>(x);
   const int pitch = mx4_pitch(cols);
   if (vec_ok(x, ld, sizeof(T)))
-    mx4_quantize_kernel<T, true><<<u.grid, kQThreads, 0, s>>>(p, ld, u.units, u.upr, u.magic, pitch, codes, scales);
-  else
-    mx4_quantize_kernel<T, false><<<u.grid, kQThreads, 0, s>>>(p, ld, u.units, u.upr, u.magic, pitch, codes, scales);
-  return cudaGetLastError();
+    return launch_dependent(mx4_quantize_kernel<T, true>, u.grid, kQThreads, 0, s, p, ld, u.units, u.upr, u.magic, pitch,
+                            codes, scales);
+  return launch_dependent(mx4_quantize_kernel<T, false>, u.grid, kQThreads, 0, s, p, ld, u.units, u.upr, u.magic, pitch,
+                          codes, scales);
 }
 
 template <typename T>
@@ -250,10 +255,10 @@ cudaError_t dequantize(const uint8_t* codes, const uint8_t* scales, int rows, in
   T* p = static_cast<T*>(out);
   const int pitch = mx4_pitch(cols);
   if (vec_ok(out, ld, sizeof(T)))
-    mx4_dequantize_kernel<T, true><<<u.grid, kQThreads, 0, s>>>(codes, scales, u.units, u.upr, u.magic, pitch, p, ld);
-  else
-    mx4_dequantize_kernel<T, false><<<u.grid, kQThreads, 0, s>>>(codes, scales, u.units, u.upr, u.magic, pitch, p, ld);
-  return cudaGetLastError();
+    return launch_dependent(mx4_dequantize_kernel<T, true>, u.grid, kQThreads, 0, s, codes, scales, u.units, u.upr, u.magic, pitch,
+                            p, ld);
+  return launch_dependent(mx4_dequantize_kernel<T, false>, u.grid, kQThreads, 0, s, codes, scales, u.units, u.upr, u.magic, pitch,
+                          p, ld);
 }
 
 }  // namespace

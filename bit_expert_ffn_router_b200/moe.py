@@ -67,7 +67,12 @@ class LayerCfg:
     hot_slots: int = 0
 
     def c(self) -> _Cfg:
-        return _Cfg(*(getattr(self, f.name) for f in dataclasses.fields(self)))
+        """The C structure (built once; the library only reads it)."""
+        c = self.__dict__.get("_struct")
+        if c is None:
+            c = _Cfg(*(getattr(self, f.name) for f in dataclasses.fields(self)))
+            object.__setattr__(self, "_struct", c)
+        return c
 
     def replace(self, **kw) -> "LayerCfg":
         return dataclasses.replace(self, **kw)
@@ -287,11 +292,21 @@ class Context:
         do the two table entries (a, b: host index arrays into the flat device table slot_of)."""
         _check(self.slot_swap_status(cfg, pool, stride, slot_of, n_slots, a, b, stream), "moe_slot_swap")
 
+    # The calls below take a few microseconds on the GPU at their smallest, so
+    # their arguments go to ctypes as plain integers, without objects around them.
+
+    def _raw_stream(self, stream) -> int:
+        """The stream's handle; None is the current stream of this context's device."""
+        if stream is not None:
+            return stream.cuda_stream
+        import torch
+        return torch._C._cuda_getCurrentRawStream(self.device)
+
     # -- the router's balance loss -------------------------------------------------
     def balance_loss_status(self, cfg, logits, idx, mask, T, stats, counts, prob, ws, stream=None) -> int:
-        return self.lib.moe_balance_loss(self.h, ctypes.byref(cfg.c()), _ptr(logits), _ptr(idx), _ptr(mask), T,
-                                         _ptr(stats), _ptr(counts), _ptr(prob), _ptr(ws),
-                                         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+        return self.lib.moe_balance_loss(self.h, ctypes.byref(cfg.c()), _adr(logits), _adr(idx), _adr(mask), T,
+                                         _adr(stats), _adr(counts), _adr(prob), _adr(ws),
+                                         0 if ws is None else ws.nbytes, self._raw_stream(stream))
 
     def balance_loss(self, cfg, logits, idx, mask, T, stats, counts, prob, ws, stream=None) -> None:
         """moe_balance_loss: stats [4] fp32 (balance loss, z loss, tokens that count, largest load), counts [E]
@@ -301,9 +316,9 @@ class Context:
 
     def balance_loss_backward_status(self, cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate, d_logits,
                                      stream=None) -> int:
-        return self.lib.moe_balance_loss_backward(self.h, ctypes.byref(cfg.c()), _ptr(logits), _ptr(idx), _ptr(gate),
-                                                  _ptr(mask), T, _ptr(stats), _ptr(counts), _ptr(d_loss),
-                                                  _ptr(d_gate), _ptr(d_logits), _stream(stream))
+        return self.lib.moe_balance_loss_backward(self.h, ctypes.byref(cfg.c()), _adr(logits), _adr(idx), _adr(gate),
+                                                  _adr(mask), T, _adr(stats), _adr(counts), _adr(d_loss),
+                                                  _adr(d_gate), _adr(d_logits), self._raw_stream(stream))
 
     def balance_loss_backward(self, cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate, d_logits,
                               stream=None) -> None:
@@ -317,8 +332,8 @@ class Context:
         rows, cols, ld = _rows(x)
         if _bad_mx4(codes, scales, rows, cols):
             return EINVAL
-        return self.lib.moe_mx4_quantize(self.h, _ptr(x), _type(x), rows, cols, ld, _ptr(codes), _ptr(scales),
-                                         _stream(stream))
+        return self.lib.moe_mx4_quantize(self.h, x.data_ptr(), _type(x), rows, cols, ld, codes.data_ptr(),
+                                         scales.data_ptr(), self._raw_stream(stream))
 
     def mx4_quantize(self, x, codes, scales, stream=None) -> None:
         """moe_mx4_quantize: x [rows, cols] (bf16, fp16 or fp32, any row stride) to codes and scales as
@@ -329,8 +344,8 @@ class Context:
         rows, cols, ld = _rows(out)
         if _bad_mx4(codes, scales, rows, cols):
             return EINVAL
-        return self.lib.moe_mx4_dequantize(self.h, _ptr(codes), _ptr(scales), rows, cols, _ptr(out), _type(out), ld,
-                                           _stream(stream))
+        return self.lib.moe_mx4_dequantize(self.h, codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
+                                           _type(out), ld, self._raw_stream(stream))
 
     def mx4_dequantize(self, codes, scales, out, stream=None) -> None:
         """moe_mx4_dequantize: the values of codes and scales to out [rows, cols] (bf16, fp16 or fp32)."""
@@ -342,13 +357,15 @@ class Context:
         x_rows = codes.shape[0]
         if _bad_mx4(codes, scales, x_rows, w.cols) or cols != (w.rows // 2 if swiglu else w.rows):
             return EINVAL
-        need = x_rows if grouping is None else grouping.n_pairs + (grouping.T if shared_slot >= 0 else 0)
+        if grouping is None:
+            need, g = x_rows, None
+        else:
+            need, g = grouping.n_pairs + (grouping.T if shared_slot >= 0 else 0), ctypes.byref(grouping)
         if rows < need:
             return EINVAL
         flags = (MX4_GATHER if gather else 0) | (MX4_SWIGLU if swiglu else 0) | (MX4_GATE if gate else 0)
-        return self.lib.moe_mx4_product(self.h, _ptr(codes), _ptr(scales), x_rows, ctypes.byref(w.c()),
-                                        None if grouping is None else ctypes.byref(grouping), shared_slot, flags,
-                                        _ptr(out), _type(out), ld, _stream(stream))
+        return self.lib.moe_mx4_product(self.h, codes.data_ptr(), scales.data_ptr(), x_rows, ctypes.byref(w.c()), g,
+                                        shared_slot, flags, out.data_ptr(), _type(out), ld, self._raw_stream(stream))
 
     def mx4_product(self, codes, scales, w: "Mx4Matrix", out, grouping=None, shared_slot=-1, gather=False,
                     swiglu=False, gate=False, stream=None) -> None:
@@ -463,23 +480,40 @@ class PreparedStack:
 
 # ------------------------------------------------------------------ 4-bit MX matrices
 
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _rows(t):
     """(rows, cols, elements from row to row) of a 2-D tensor with contiguous rows."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise MoeError(EINVAL, f"a 2-D tensor with contiguous rows is needed, got {tuple(t.shape)}, {t.stride()}")
-    return t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        rows, cols = shape
+        if rows <= 1 and (cols <= 1 or stride[1] == 1):
+            return rows, cols, cols
+        if (cols <= 1 or stride[1] == 1) and stride[0] >= cols:
+            return rows, cols, stride[0]
+    raise MoeError(EINVAL, f"a 2-D tensor with contiguous rows is needed, got {tuple(shape)}, {stride}")
+
+
+_type_codes = {}
 
 
 def _type(t) -> int:
-    import torch
-    return {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}.get(t.dtype, -1)
+    if not _type_codes:
+        import torch
+        _type_codes.update({torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32})
+    return _type_codes.get(t.dtype, -1)
 
 
 def _bad_mx4(codes, scales, rows, cols) -> bool:
-    """Whether codes and scales are not the contiguous bytes of [rows, cols] MX rows."""
-    pitch = mx4_scale_pitch(cols)
-    return any(t.element_size() != 1 or not t.is_contiguous() or tuple(t.shape) != (rows, n)
-               for t, n in ((codes, cols // 2), (scales, pitch))) if pitch else False
+    """Whether codes and scales are not the contiguous bytes of [rows, cols] MX rows (a number of columns
+    that no MX row has is left to the library to refuse)."""
+    if cols <= 0 or cols % MX4_BLOCK:
+        return False
+    return (codes.shape != (rows, cols // 2) or scales.shape != (rows, (cols // MX4_BLOCK + 15) // 16 * 16)
+            or codes.element_size() != 1 or scales.element_size() != 1
+            or not codes.is_contiguous() or not scales.is_contiguous())
 
 
 def mx4_scale_pitch(cols: int) -> int:
