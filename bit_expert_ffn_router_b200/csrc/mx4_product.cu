@@ -64,9 +64,7 @@ static_assert(Smem::kStage % 1024 == 0, "swizzle atoms start on 1024 bytes");
 
 // The groups' row tiles, laid end to end: group i's first is prefix[i].
 struct Table {
-  uint64_t full[kStages];      // TMA (tx): codes landed
-  uint64_t x_full[kStages];    // gather threads (count 128): x rows landed, where tokens name them
-  uint64_t sf_full[kStages];   // scale threads (count 128)
+  uint64_t full[kStages];      // TMA (tx), scale warps, gather warps: a stage is complete
   uint64_t empty[kStages];     // MMA commit: codes and scales read
   uint64_t d_full[2];          // MMA commit: accumulator complete
   uint64_t d_empty[2];         // epilogue (count 256)
@@ -246,6 +244,20 @@ __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a, uint64_
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Every lane's shared-memory writes, made visible to the asynchronous units
+// that read them, then one arrival for the warp.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  fence_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // The scale bytes of blocks 16 pair .. 16 pair + 15 of one row as four words
 // (blocks past the row's end read as 0).
 __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pair, int blocks) {
@@ -346,9 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&B->full[i], 1);
-      mbar_init(&B->x_full[i], kGatherThreads);
-      mbar_init(&B->sf_full[i], kScaleThreads);
+      mbar_init(&B->full[i], 1 + kScaleThreads / 32 + (P.gather ? kGatherThreads / 32 : 0));
       mbar_init(&B->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -403,46 +413,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      int g = 0, i = 0;
-      for (int w = blockIdx.x; w < total; w += G, ++i) {
-        const Item it = item_at(P, *B, w);
-        const uint32_t id0 = instr_desc_mxf4(it.n16, 0), id1 = instr_desc_mxf4(it.n16, 1);
-        const int acc = i & 1;
-        if (i >= 2 && !wait_bar(B, &B->d_empty[acc], ((i >> 1) - 1) & 1, P, 2)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * kAcc);
-        bool ok = true;
-        for (int k = 0; k < n_k; ++k, ++g) {
-          const int st = g % kStages;
-          const uint32_t ph = (g / kStages) & 1;
-          if (!wait_bar(B, &B->full[st], ph, P, 3) || !wait_bar(B, &B->sf_full[st], ph, P, 4) ||
-              (P.gather && !wait_bar(B, &B->x_full[st], ph, P, 7))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint8_t* stage = smem + st * Smem::kStage;
-          const uint32_t sf = tmem + static_cast<uint32_t>(2 * kAcc + st * kSfCols);
-          const int steps = min((P.K - k * kBK + 63) / 64, 4);
-          for (int h = 0; h < (steps > 2 ? 2 : 1); ++h) {
-            tc_copy_scales(sf + 4 * h, scale_desc(stage + Smem::kSfA + 512 * h));
-            tc_copy_scales(sf + 8 + 8 * h, scale_desc(stage + Smem::kSfB + 1024 * h));
-            if (it.n16 > 128) tc_copy_scales(sf + 12 + 8 * h, scale_desc(stage + Smem::kSfB + 1024 * h + 512));
-          }
-          const uint64_t da = smem_desc(stage + Smem::kA), db = smem_desc(stage + Smem::kB);
-          for (int s = 0; s < steps; ++s)  // K = 64 per MMA: 32 bytes of a row
-            tc_mma_mxf4(d_tmem, da + 2 * s, db + 2 * s, (s & 1) ? id1 : id0, sf + 4 * (s >> 1), sf + 8 + 8 * (s >> 1),
-                        (k > 0 || s > 0) ? 1u : 0u);
-          tc_commit(&B->empty[st]);
+    // The whole warp walks the loop and one lane issues: the operands then stay
+    // in uniform registers, and a stage costs the issuer less than its MMAs take.
+    const uint64_t da0 = smem_desc(smem + Smem::kA), db0 = smem_desc(smem + Smem::kB);
+    const uint64_t sa0 = scale_desc(smem + Smem::kSfA), sb0 = scale_desc(smem + Smem::kSfB);
+    int st = 0, i = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; w < total && ok; w += G, ++i) {
+      const Item it = item_at(P, *B, w);
+      const uint32_t id0 = instr_desc_mxf4(it.n16, 0), id1 = instr_desc_mxf4(it.n16, 1);
+      const bool wide = it.n16 > 128;
+      const int acc = i & 1;
+      if (i >= 2 && !wait_bar(B, &B->d_empty[acc], ((i >> 1) - 1) & 1, P, 2)) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * kAcc);
+      for (int k = 0; k < n_k; ++k) {
+        if (!wait_bar(B, &B->full[st], ph, P, 3)) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
-        tc_commit(&B->d_full[acc]);
+        tc_fence_after();
+        const uint64_t off = static_cast<uint64_t>(st * (Smem::kStage >> 4));
+        const uint32_t sf = tmem + static_cast<uint32_t>(2 * kAcc + st * kSfCols);
+        const int steps = P.K - k * kBK;  // K values left
+        if (elect_one()) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1 && steps <= 128) break;
+            tc_copy_scales(sf + 4 * h, sa0 + off + 32 * h);
+            tc_copy_scales(sf + 8 + 8 * h, sb0 + off + 64 * h);
+            if (wide) tc_copy_scales(sf + 12 + 8 * h, sb0 + off + 64 * h + 32);
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s)  // K = 64 per MMA: 32 bytes of a row
+            if (64 * s < steps)
+              tc_mma_mxf4(d_tmem, da0 + off + 2 * s, db0 + off + 2 * s, (s & 1) ? id1 : id0, sf + 4 * (s >> 1),
+                          sf + 8 + 8 * (s >> 1), (k > 0 || s > 0) ? 1u : 0u);
+          tc_commit(&B->empty[st]);
+          if (k == n_k - 1) tc_commit(&B->d_full[acc]);
+        }
+        __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
       }
-      // everything issued above completes before the tensor memory is freed
-      tc_commit(&B->mma_done);
-      mbar_wait(&B->mma_done, 0, global_timer_ns() + P.timeout_ns);
     }
+    // everything issued above completes before the tensor memory is freed
+    if (elect_one()) tc_commit(&B->mma_done);
+    __syncwarp();
+    if (lane == 0) mbar_wait(&B->mma_done, 0, global_timer_ns() + P.timeout_ns);
+    __syncwarp();
   } else if (warp < 6) {
     // ---------------------------------------------------------- scales
     const int r = threadIdx.x - 64;
@@ -493,8 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             put_scales(stage + Smem::kSfB + 1024 * h, r, w1);
             if (it.n16 > 128) put_scales(stage + Smem::kSfB + 1024 * h + 512, r, w2);
           }
-          fence_async_smem();  // the stores above are read by the asynchronous scale copies
-          mbar_arrive(&B->sf_full[st]);
+          arrive_warp(&B->full[st]);  // the stores above are read by the asynchronous scale copies
           ++g;
         }
       }
@@ -534,15 +555,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("cp.async.commit_group;" ::: "memory");
           if (g - told >= kGatherLag) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kGatherLag) : "memory");
-            fence_async_smem();
-            mbar_arrive(&B->x_full[told % kStages]);
+            arrive_warp(&B->full[told % kStages]);
             ++told;
           }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_async_smem();
-      for (; told < g; ++told) mbar_arrive(&B->x_full[told % kStages]);
+      for (; told < g; ++told) arrive_warp(&B->full[told % kStages]);
     }
   } else {
     // ---------------------------------------------------------- epilogue
