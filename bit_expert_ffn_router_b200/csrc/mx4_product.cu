@@ -36,36 +36,23 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 576;
-constexpr int kBM = 128;                      // weight rows per tile
-constexpr int kBN = 208;                      // x rows per tile, at most
+// warps by role
+constexpr int kWarpScales = 2, kScaleWarps = 3;
+constexpr int kWarpEpi = kWarpScales + kScaleWarps, kEpiWarps = 8;
+constexpr int kWarpGather = kWarpEpi + kEpiWarps, kGatherWarps = 4;
+constexpr int kThreads = 32 * (kWarpGather + kGatherWarps);
 constexpr int kBK = 256;                      // K values per stage: 128 bytes of codes per row
-constexpr int kStages = 4;
 constexpr int kMaxGroups = kMaxE + 1;
-constexpr int kAcc = kBN;                     // TMEM columns of one accumulator
-constexpr int kSfCols = 24;                   // TMEM columns of a stage's scales: w 2 x 4, x 2 x 8
-static_assert(2 * kAcc + kStages * kSfCols <= 512, "tensor memory budget");
-constexpr int kScaleThreads = 128;
-constexpr int kEpiThreads = 256;
-constexpr int kGatherThreads = 128;
-constexpr int kGatherRows = kBN / (kGatherThreads / 8);  // rows of a stage per gather thread
-constexpr int kGatherLag = 2;                            // stages between issuing a copy and announcing it
+constexpr int kList = 256;                    // items of a CTA worked out at its start
+constexpr int kGatherThreads = 32 * kGatherWarps;
 constexpr int kBoxA = 64, kBoxB = 16;                    // x rows of the two TMA boxes
 
-struct Smem {
-  static constexpr int kA = 0;                          // kBM rows x 128 bytes, 128B-swizzled
-  static constexpr int kB = kBM * 128;                  // kBN rows x 128 bytes
-  static constexpr int kSfA = kB + kBN * 128;           // 2 pieces of 512 bytes (K 0..127, 128..255)
-  static constexpr int kSfB = kSfA + 1024;              // 2 x 2 pieces (K half, rows 0..127 / 128..255)
-  static constexpr int kStage = kSfB + 2048;
-  static constexpr int kTable = kStages * kStage;
-};
-static_assert(Smem::kStage % 1024 == 0, "swizzle atoms start on 1024 bytes");
+constexpr int kMaxStages = 7;
 
 // The groups' row tiles, laid end to end: group i's first is prefix[i].
 struct Table {
-  uint64_t full[kStages];      // TMA (tx), scale warps, gather warps: a stage is complete
-  uint64_t empty[kStages];     // MMA commit: codes and scales read
+  uint64_t full[kMaxStages];   // TMA (tx), scale warps, gather warps: a stage is complete
+  uint64_t empty[kMaxStages];  // MMA commit: codes and scales read
   uint64_t d_full[2];          // MMA commit: accumulator complete
   uint64_t d_empty[2];         // epilogue (count 256)
   uint64_t mma_done;
@@ -77,20 +64,48 @@ struct Table {
   int first[kMaxGroups];
   int rows[kMaxGroups];
   int slot[kMaxGroups];
+  alignas(16) int4 list[kList];
 };
-constexpr int kSmemBytes = Smem::kTable + static_cast<int>(sizeof(Table)) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+
+// Sizes for tiles of at most BM x rows and BN weight rows, in a ring of STAGES
+// stages. The MMA always takes 128 x rows: with BM = 64 the upper half reads
+// what follows in shared memory, and nobody reads its results.
+template <int BM, int BN, int STAGES>
+struct Shape {
+  static constexpr int kBM = BM;
+  static constexpr int kBN = BN;
+  static constexpr int kStages = STAGES;
+  static constexpr int kAcc = BN;                               // TMEM columns of one accumulator
+  static constexpr int kPieces = (BN + 127) / 128;              // of 128 weight rows
+  static constexpr int kSfCols = 8 + 8 * kPieces;               // TMEM columns of a stage's scales
+  static constexpr int kGatherRows = BM / (kGatherThreads / 8); // rows of a stage per gather thread
+  // a stage in shared memory
+  static constexpr int kX = 0;                          // BM rows x 128 bytes, 128B-swizzled
+  static constexpr int kW = BM * 128;                   // BN rows x 128 bytes
+  static constexpr int kSfX = kW + BN * 128;            // 2 pieces of 512 bytes (K 0..127, 128..255)
+  static constexpr int kSfW = kSfX + 1024;              // 2 x kPieces pieces (K half, 128 weight rows)
+  static constexpr int kStage = kSfW + 1024 * kPieces;
+  static constexpr int kOut = STAGES * kStage;          // 32 rows x 128 bytes for each epilogue warp
+  static constexpr int kTable = kOut + kEpiWarps * 4096;
+  static constexpr int kSmem = kTable + static_cast<int>(sizeof(Table)) + 1024;
+  static_assert(kStage % 1024 == 0 && kW % 1024 == 0, "swizzle atoms start on 1024 bytes");
+  static_assert(BM == 128 || BM * 128 + BN * 128 >= 128 * 128, "128 x rows lie inside the stage");
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(STAGES <= kMaxStages && 2 * kAcc + STAGES * kSfCols <= 512, "tensor memory budget");
+};
+using Wide = Shape<128, 192, 4>;
+using Narrow = Shape<64, 128, 6>;
 
 struct Params {
   const uint8_t *xc, *xs, *ws;  // x codes; scales
   size_t ws_stride;
-  int x_rows, w_rows, n_slots, K, pitch, m_tiles;
+  int x_rows, w_rows, n_slots, K, pitch, w_tiles;
   bool grouped;
   const int32_t *n_uniq, *uniq_offset, *uniq_slot, *pair_token;
   const float* pair_gate;
   int n_pairs, T, max_uniq, shared_slot;
   bool gather, gate;
-  bool pack;               // 32-bit stores of two neighbouring 16-bit results
+  int vec;                 // bytes that every output row is aligned to: 32, 16 or less
   void* out;
   long long ld;
   int* status;
@@ -120,8 +135,12 @@ __device__ __forceinline__ bool wait_warp(Table* B, uint64_t* bar, uint32_t pari
   return ok != 0;
 }
 
-__device__ __forceinline__ int tiles_of(int rows) { return (rows + kBN - 1) / kBN; }
+template <typename S>
+__device__ __forceinline__ int tiles_of(int rows) {
+  return (rows + S::kBM - 1) / S::kBM;
+}
 
+template <typename Sh>
 __device__ void build_table(const Params& P, Table& S) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nu = P.grouped ? min(max(__ldg(P.n_uniq), 0), P.max_uniq) : 0;
@@ -148,7 +167,7 @@ __device__ void build_table(const Params& P, Table& S) {
     S.rows[i] = n;
     S.slot[i] = slot;
     S.prefix[i] = mine;
-    mine += tiles_of(n);
+    mine += tiles_of<Sh>(n);
   }
   int incl = mine;
 #pragma unroll
@@ -168,14 +187,16 @@ __device__ void build_table(const Params& P, Table& S) {
 }
 
 struct Item {
-  int m, row0, rows, slot, n16;
+  int n0, row0, rows, slot;  // first weight row; first output row and their number; pool slot
+  __device__ __forceinline__ int rows16() const { return (rows + 15) & ~15; }
 };
 
-// Item w: tile w / m_tiles of weight tile w % m_tiles. The group is the last
-// one whose first tile is at most the tile (empty groups share the next
+// Item w: row tile w / w_tiles with weight tile w % w_tiles. The group is the
+// last one whose first tile is at most the tile (empty groups share the next
 // one's); its rows are cut into equal tiles of a multiple of 16.
-__device__ __forceinline__ Item item_at(const Params& P, const Table& S, int w) {
-  const int tile = w / P.m_tiles;
+template <typename Sh>
+__device__ Item work_out(const Params& P, const Table& S, int w) {
+  const int tile = w / P.w_tiles;
   int lo = 0, hi = S.n_groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -184,15 +205,22 @@ __device__ __forceinline__ Item item_at(const Params& P, const Table& S, int w) 
     else
       hi = mid;
   }
-  const int n = S.rows[lo], nt = tiles_of(n), j = tile - S.prefix[lo];
+  const int n = S.rows[lo], nt = tiles_of<Sh>(n), j = tile - S.prefix[lo];
   const int tr = ((n + nt - 1) / nt + 15) & ~15;
   Item it;
-  it.m = w - tile * P.m_tiles;
+  it.n0 = (w - tile * P.w_tiles) * Sh::kBN;
   it.row0 = S.first[lo] + j * tr;
   it.rows = min(tr, n - j * tr);
   it.slot = S.slot[lo];
-  it.n16 = (it.rows + 15) & ~15;
   return it;
+}
+
+// This CTA's i-th item, blockIdx.x + i * gridDim.x.
+template <typename Sh>
+__device__ __forceinline__ Item item_at(const Params& P, const Table& S, int i) {
+  if (i >= kList) return work_out<Sh>(P, S, blockIdx.x + i * gridDim.x);
+  const int4 v = S.list[i];
+  return {v.x, v.y, v.z, v.w};
 }
 
 // x row of output row p; out-of-range tokens are clamped (and reported by the
@@ -274,10 +302,6 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pair, int b
   return v;
 }
 
-__device__ __forceinline__ void put_scales(uint8_t* piece, int row, uint32_t word) {
-  *reinterpret_cast<uint32_t*>(piece + (row & 31) * 16 + (row >> 5) * 4) = word;
-}
-
 template <typename T>
 __device__ __forceinline__ T narrow(float v);
 template <>
@@ -287,6 +311,13 @@ __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_
 template <>
 __device__ __forceinline__ float narrow<float>(float v) { return v; }
 
+// 1 / x of x in [1, infinity], within a step (0 above 2^126).
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   T v[2] = {narrow<T>(a), narrow<T>(b)};
@@ -295,75 +326,107 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return r;
 }
 
-// 16 accumulator columns (output rows p0 .. p0 + 15, `left` of them real) of
-// weight row wr in v; lane i holds the gate of row p0 + i % 16.
+// Words 8i .. 8i + 7 as one 32-byte store, a whole sector of this lane's row.
+__device__ __forceinline__ void store32(uint32_t* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// 16 accumulator columns of one output row (weight rows n .. n + 15) in v to
+// `words` 32-bit words of results.
 template <typename T, bool SWIGLU>
-__device__ __forceinline__ void store16(const Params& P, const float* v, int wr, long long p0, int left, float gate_l) {
-  const bool live = wr < P.w_rows;
-  T* out = static_cast<T*>(P.out) + p0 * P.ld;
-  if constexpr (!SWIGLU && sizeof(T) == 4) {
-    float o[16];
+__device__ __forceinline__ void results16(const float* v, float gate, uint32_t* words) {
+  constexpr int kN = SWIGLU ? 8 : 16;
+  float o[kN];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = P.gate ? v[i] * __shfl_sync(0xffffffffu, gate_l, i) : v[i];
+  for (int i = 0; i < kN; ++i) {
+    // h is rounded to 16 bits or summed in fp32 far above these errors: the
+    // fast exponential and reciprocal (2 + 1.2 |v| steps, 1 step)
+    if (SWIGLU)
+      o[i] = v[2 * i] * fast_rcp(1.f + __expf(-v[2 * i])) * v[2 * i + 1] * gate;
+    else
+      o[i] = v[i] * gate;
+  }
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (live && i < left) out[i * P.ld + wr] = narrow<T>(o[i]);
+    for (int i = 0; i < kN; ++i) words[i] = __float_as_uint(o[i]);
   } else {
-    // Neighbouring lanes hold rows 2c and 2c + 1 of w; of every two columns the
-    // even lane takes the first with both rows, the odd lane the second.
-    const int odd = threadIdx.x & 1;
-    float a[8], b[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
-      a[i] = odd ? other : v[2 * i];
-      b[i] = odd ? v[2 * i + 1] : other;
-      // h is rounded to 16 bits or summed in fp32 far above these errors: the
-      // fast exponential and division (2 + 1.2 |a| steps, 2 steps)
-      if (SWIGLU) a[i] = __fdividef(a[i], 1.f + __expf(-a[i])) * b[i];
-      if (P.gate) {
-        const float g = __shfl_sync(0xffffffffu, gate_l, 2 * i + odd);
-        a[i] *= g, b[i] *= g;
-      }
-    }
-    out += odd * P.ld + (SWIGLU ? wr >> 1 : wr & ~1);
-    left -= odd;
-    if (SWIGLU) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (live && 2 * i < left) out[2 * i * P.ld] = narrow<T>(a[i]);
-    } else if (P.pack) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (live && 2 * i < left) *reinterpret_cast<uint32_t*>(out + 2 * i * P.ld) = pack2<T>(a[i], b[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (live && 2 * i < left) {
-          out[2 * i * P.ld] = narrow<T>(a[i]);
-          out[2 * i * P.ld + 1] = narrow<T>(b[i]);
-        }
-    }
+    for (int i = 0; i < kN / 2; ++i) words[i] = pack2<T>(o[2 * i], o[2 * i + 1]);
   }
 }
 
-template <typename T, bool SWIGLU>
+// N words to p, aligned to `vec` bytes.
+template <typename T, int N>
+__device__ __forceinline__ void store_words(T* p, const uint32_t* w, int vec) {
+  if (N % 8 == 0 && vec >= 32) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) store32(reinterpret_cast<uint32_t*>(p) + i, w + i);
+  } else if (vec >= 16) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else {
+    T v[N * 4 / sizeof(T)];
+    memcpy(v, w, N * 4);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(N * 4 / sizeof(T)); ++i) p[i] = v[i];
+  }
+}
+
+// A lane's own row, without staging: `valid` of N words.
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* p, const uint32_t* w, int valid, int vec) {
+  if (valid == N)
+    store_words<T, N>(p, w, vec);
+  else
+    store_words<T, N / 2>(p, w, vec);
+}
+
+// 32 rows of `valid` of N words (lane l has row l's, `rows` rows are real) to
+// p, ld elements from row to row, through the warp's shared memory, so that a
+// store covers 64 or 128 bytes of a row by neighbouring lanes (16 bytes each;
+// the units are swizzled against bank conflicts). Stores of a row per lane
+// instead: fp32 rows of a down product 15% slower.
+template <typename T, int N>
+__device__ __forceinline__ void store_staged(uint4* stage, const uint32_t* w, T* p, long long ld, int rows, int valid) {
+  constexpr int kUnits = N / 4, kRowsAtOnce = 32 / kUnits;
+  const int lane = threadIdx.x & 31, u = lane % kUnits;
+  auto place = [&](int row, int unit) {
+    return stage + row * kUnits + (unit ^ (kUnits == 8 ? row & 7 : (row >> 1) & (kUnits - 1)));
+  };
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) *place(lane, i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  __syncwarp();
+  p += (lane / kUnits) * ld + u * (16 / static_cast<int>(sizeof(T)));
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k, p += kRowsAtOnce * ld) {
+    const int row = k * kRowsAtOnce + lane / kUnits;
+    if (row < rows && 4 * u < valid) *reinterpret_cast<uint4*>(p) = *place(row, u);
+  }
+}
+
+template <typename Sh, typename T, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
     mx4_product_kernel(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tXa,
                        const __grid_constant__ CUtensorMap tXb, const Params P) {
+  constexpr int kStages = Sh::kStages, kAcc = Sh::kAcc, kGatherRows = Sh::kGatherRows,
+                kPieces = Sh::kPieces;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Table* B = reinterpret_cast<Table*>(smem + Smem::kTable);
+  Table* B = reinterpret_cast<Table*>(smem + Sh::kTable);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&B->full[i], 1 + kScaleThreads / 32 + (P.gather ? kGatherThreads / 32 : 0));
+      mbar_init(&B->full[i], 1 + kScaleWarps + (P.gather ? kGatherWarps : 0));
       mbar_init(&B->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->d_full[i], 1);
-      mbar_init(&B->d_empty[i], kEpiThreads);
+      mbar_init(&B->d_empty[i], 32 * kEpiWarps);
     }
     mbar_init(&B->mma_done, 1);
     B->abort_flag = 0;
@@ -371,38 +434,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc(&B->tmem_base, 512);
   grid_dep_wait();  // codes, scales and grouping come from the kernels before this one
-  build_table(P, *B);
+  build_table<Sh>(P, *B);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem_base;
-  const int total = B->prefix[B->n_groups] * P.m_tiles;
+  const int total = B->prefix[B->n_groups] * P.w_tiles;
+  const int n_items = total > static_cast<int>(blockIdx.x) ? (total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+  for (int i = threadIdx.x; i < min(n_items, kList); i += kThreads) {
+    const Item it = work_out<Sh>(P, *B, blockIdx.x + i * gridDim.x);
+    B->list[i] = make_int4(it.n0, it.row0, it.rows, it.slot);
+  }
+  __syncthreads();
   const int n_k = (P.K + kBK - 1) / kBK;
-  const int G = gridDim.x;
 
   if (warp == 0) {
     // ---------------------------------------------------------- codes
     int g = 0;
     if (lane == 0) {
       bool ok = true;
-      for (int w = blockIdx.x; w < total && ok; w += G) {
-        const Item it = item_at(P, *B, w);
-        const uint32_t tx = static_cast<uint32_t>(kBM + (P.gather ? 0 : it.n16)) * 128u;
+      for (int i = 0; i < n_items && ok; ++i) {
+        const Item it = item_at<Sh>(P, *B, i);
+        const uint32_t tx = static_cast<uint32_t>(Sh::kBN + (P.gather ? 0 : it.rows16())) * 128u;
         for (int k = 0; k < n_k; ++k, ++g) {
           const int st = g % kStages;
           if (g >= kStages && !wait_bar(B, &B->empty[st], ((g / kStages) - 1) & 1, P, 1)) {
             ok = false;
             break;
           }
-          uint8_t* stage = smem + st * Smem::kStage;
+          uint8_t* stage = smem + st * Sh::kStage;
           mbar_arrive_expect_tx(&B->full[st], tx);
-          tma_load_3d(stage + Smem::kA, &tW, k * (kBK / 2), it.m * kBM, it.slot, &B->full[st]);
+          tma_load_3d(stage + Sh::kW, &tW, k * (kBK / 2), it.n0, it.slot, &B->full[st]);
           if (P.gather) continue;
-          int r = 0;  // n16 rows: boxes of 64, the rest in boxes of 16
-          for (; r + kBoxA <= it.n16; r += kBoxA)
-            tma_load_2d(stage + Smem::kB + r * 128, &tXa, k * (kBK / 2), it.row0 + r, &B->full[st]);
-          for (; r < it.n16; r += kBoxB)
-            tma_load_2d(stage + Smem::kB + r * 128, &tXb, k * (kBK / 2), it.row0 + r, &B->full[st]);
+          int r = 0;  // boxes of 64 rows, the rest in boxes of 16
+          for (; r + kBoxA <= it.rows16(); r += kBoxA)
+            tma_load_2d(stage + Sh::kX + r * 128, &tXa, k * (kBK / 2), it.row0 + r, &B->full[st]);
+          for (; r < it.rows16(); r += kBoxB)
+            tma_load_2d(stage + Sh::kX + r * 128, &tXb, k * (kBK / 2), it.row0 + r, &B->full[st]);
         }
       }
     }
@@ -415,15 +483,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- MMA issue
     // The whole warp walks the loop and one lane issues: the operands then stay
     // in uniform registers, and a stage costs the issuer less than its MMAs take.
-    const uint64_t da0 = smem_desc(smem + Smem::kA), db0 = smem_desc(smem + Smem::kB);
-    const uint64_t sa0 = scale_desc(smem + Smem::kSfA), sb0 = scale_desc(smem + Smem::kSfB);
-    int st = 0, i = 0;
+    const uint64_t da0 = smem_desc(smem + Sh::kX), db0 = smem_desc(smem + Sh::kW);
+    const uint64_t sa0 = scale_desc(smem + Sh::kSfX), sb0 = scale_desc(smem + Sh::kSfW);
+    int st = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int w = blockIdx.x; w < total && ok; w += G, ++i) {
-      const Item it = item_at(P, *B, w);
-      const uint32_t id0 = instr_desc_mxf4(it.n16, 0), id1 = instr_desc_mxf4(it.n16, 1);
-      const bool wide = it.n16 > 128;
+    for (int i = 0; i < n_items && ok; ++i) {
+      const Item it = item_at<Sh>(P, *B, i);
+      const int n = min(Sh::kBN, P.w_rows - it.n0);
+      const uint32_t id0 = instr_desc_mxf4(n, 0), id1 = instr_desc_mxf4(n, 1);
       const int acc = i & 1;
       if (i >= 2 && !wait_bar(B, &B->d_empty[acc], ((i >> 1) - 1) & 1, P, 2)) break;
       tc_fence_after();
@@ -434,22 +502,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint64_t off = static_cast<uint64_t>(st * (Smem::kStage >> 4));
-        const uint32_t sf = tmem + static_cast<uint32_t>(2 * kAcc + st * kSfCols);
+        const uint64_t off = static_cast<uint64_t>(st * (Sh::kStage >> 4));
+        const uint32_t sf = tmem + static_cast<uint32_t>(2 * kAcc + st * Sh::kSfCols);
         const int steps = P.K - k * kBK;  // K values left
         if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == 1 && steps <= 128) break;
             tc_copy_scales(sf + 4 * h, sa0 + off + 32 * h);
-            tc_copy_scales(sf + 8 + 8 * h, sb0 + off + 64 * h);
-            if (wide) tc_copy_scales(sf + 12 + 8 * h, sb0 + off + 64 * h + 32);
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j)
+              tc_copy_scales(sf + 8 + 4 * (kPieces * h + j), sb0 + off + 32 * (kPieces * h + j));
           }
 #pragma unroll
           for (int s = 0; s < 4; ++s)  // K = 64 per MMA: 32 bytes of a row
             if (64 * s < steps)
               tc_mma_mxf4(d_tmem, da0 + off + 2 * s, db0 + off + 2 * s, (s & 1) ? id1 : id0, sf + 4 * (s >> 1),
-                          sf + 8 + 8 * (s >> 1), (k > 0 || s > 0) ? 1u : 0u);
+                          sf + 8 + 4 * kPieces * (s >> 1), (k > 0 || s > 0) ? 1u : 0u);
           tc_commit(&B->empty[st]);
           if (k == n_k - 1) tc_commit(&B->d_full[acc]);
         }
@@ -465,35 +534,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_wait(&B->mma_done, 0, global_timer_ns() + P.timeout_ns);
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < kWarpEpi) {
     // ---------------------------------------------------------- scales
-    const int r = threadIdx.x - 64;
+    // The first warp: the x rows'; the others: weight rows 0 .. 127, 128 .. 255.
+    // Lane l loads the scales of rows l, l + 32, l + 64, l + 96 for 16 K blocks
+    // (two stages) and stores, for each piece of 4 blocks, the four rows' words
+    // side by side.
+    const int part = warp - kWarpScales;
     const int blocks = P.K / kBlock;
     int g = 0;
     bool ok = true;
-    for (int w = blockIdx.x; w < total && ok; w += G) {
-      const Item it = item_at(P, *B, w);
-      const int wr = it.m * kBM + r;
-      const uint8_t* rows[3] = {nullptr, nullptr, nullptr};
-      if (wr < P.w_rows)
-        rows[0] = P.ws + static_cast<size_t>(it.slot) * P.ws_stride + static_cast<size_t>(wr) * P.pitch;
+    for (int i = 0; i < n_items && ok; ++i) {
+      const Item it = item_at<Sh>(P, *B, i);
+      const bool any = part <= kPieces;
+      const uint8_t* rows[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = r + 128 * h;
-        if (i >= it.rows) continue;
-        const int p = it.row0 + i;
-        if (P.gather && it.m == 0 && p < P.n_pairs &&
-            static_cast<unsigned>(__ldg(P.pair_token + p)) >= static_cast<unsigned>(P.x_rows))
-          report(P.status, kDevBadExpert, p);
-        rows[1 + h] = P.xs + static_cast<size_t>(source_row(P, p)) * P.pitch;
+      for (int j = 0; j < 4; ++j) {
+        rows[j] = nullptr;
+        const int r = lane + 32 * j;
+        if (part > 0) {
+          const int wr = it.n0 + 128 * (part - 1) + r;
+          if (any && wr < P.w_rows)
+            rows[j] = P.ws + static_cast<size_t>(it.slot) * P.ws_stride + static_cast<size_t>(wr) * P.pitch;
+        } else if (r < it.rows) {
+          const int p = it.row0 + r;
+          if (P.gather && it.n0 == 0 && p < P.n_pairs &&
+              static_cast<unsigned>(__ldg(P.pair_token + p)) >= static_cast<unsigned>(P.x_rows))
+            report(P.status, kDevBadExpert, p);
+          rows[j] = P.xs + static_cast<size_t>(source_row(P, p)) * P.pitch;
+        }
       }
-      uint4 next[3];
+      uint4 next[4];
 #pragma unroll
-      for (int j = 0; j < 3; ++j) next[j] = rows[j] != nullptr ? load_scales(rows[j], 0, blocks) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 4; ++j) next[j] = rows[j] != nullptr ? load_scales(rows[j], 0, blocks) : make_uint4(0, 0, 0, 0);
       for (int pair = 0; 2 * pair < n_k && ok; ++pair) {
-        uint4 cur[3];
+        uint4 cur[4];
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
+        for (int j = 0; j < 4; ++j) {
           cur[j] = next[j];
           if (rows[j] != nullptr && 2 * pair + 2 < n_k) next[j] = load_scales(rows[j], pair + 1, blocks);
         }
@@ -505,38 +582,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          uint8_t* stage = smem + st * Smem::kStage;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t wa = s == 0 ? (h == 0 ? cur[0].x : cur[0].y) : (h == 0 ? cur[0].z : cur[0].w);
-            const uint32_t w1 = s == 0 ? (h == 0 ? cur[1].x : cur[1].y) : (h == 0 ? cur[1].z : cur[1].w);
-            const uint32_t w2 = s == 0 ? (h == 0 ? cur[2].x : cur[2].y) : (h == 0 ? cur[2].z : cur[2].w);
-            put_scales(stage + Smem::kSfA + 512 * h, r, wa);
-            put_scales(stage + Smem::kSfB + 1024 * h, r, w1);
-            if (it.n16 > 128) put_scales(stage + Smem::kSfB + 1024 * h + 512, r, w2);
+          if (any) {
+            uint8_t* stage = smem + st * Sh::kStage;
+            uint4* p0 = reinterpret_cast<uint4*>(stage + (part == 0 ? Sh::kSfX : Sh::kSfW + 512 * (part - 1))) + lane;
+            uint4* p1 = p0 + (part == 0 ? 512 : 512 * kPieces) / 16;
+            if (s == 0) {
+              *p0 = make_uint4(cur[0].x, cur[1].x, cur[2].x, cur[3].x);
+              *p1 = make_uint4(cur[0].y, cur[1].y, cur[2].y, cur[3].y);
+            } else {
+              *p0 = make_uint4(cur[0].z, cur[1].z, cur[2].z, cur[3].z);
+              *p1 = make_uint4(cur[0].w, cur[1].w, cur[2].w, cur[3].w);
+            }
           }
           arrive_warp(&B->full[st]);  // the stores above are read by the asynchronous scale copies
           ++g;
         }
       }
     }
-  } else if (warp >= 14) {
+  } else if (warp >= kWarpGather) {
     // ---------------------------------------------------------- gathered x rows
     // Thread i copies 16-byte chunk i % 8 of rows i / 8, i / 8 + 16, ... of a
     // stage to its swizzled place (chunk ^ row % 8).
     if (P.gather) {
-      const int c = threadIdx.x & 7, r0 = (threadIdx.x - 448) >> 3;
-      const uint32_t dst0 = smem_u32(smem + Smem::kB) + static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
+      const int c = threadIdx.x & 7, r0 = (threadIdx.x - 32 * kWarpGather) >> 3;
+      const uint32_t dst0 = smem_u32(smem + Sh::kX) + static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
       const int row_b = P.K / 2;
-      int g = 0, told = 0;
+      int g = 0;
       bool ok = true;
-      for (int w = blockIdx.x; w < total && ok; w += G) {
-        const Item it = item_at(P, *B, w);
+      for (int i = 0; i < n_items && ok; ++i) {
+        const Item it = item_at<Sh>(P, *B, i);
         int src[kGatherRows];
 #pragma unroll
         for (int j = 0; j < kGatherRows; ++j) {
           const int r = r0 + 16 * j;
-          src[j] = r < it.n16 ? source_row(P, it.row0 + min(r, it.rows - 1)) : 0;
+          src[j] = r < it.rows ? source_row(P, it.row0 + r) : 0;
         }
         for (int k = 0; k < n_k; ++k, ++g) {
           const int st = g % kStages;
@@ -547,46 +626,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = k * (kBK / 2) + c * 16;
           const bool live = col < row_b;
           const uint8_t* base = P.xc + (live ? col : 0);
-          const uint32_t dst = dst0 + static_cast<uint32_t>(st * Smem::kStage);
+          const uint32_t dst = dst0 + static_cast<uint32_t>(st * Sh::kStage);
 #pragma unroll
           for (int j = 0; j < kGatherRows; ++j)
-            if (r0 + 16 * j < it.n16)
+            if (r0 + 16 * j < it.rows)
               copy16(dst + j * 16 * 128, base + static_cast<size_t>(src[j]) * row_b, live);
+          // stage g - 1 is announced once this one is on its way
           asm volatile("cp.async.commit_group;" ::: "memory");
-          if (g - told >= kGatherLag) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kGatherLag) : "memory");
-            arrive_warp(&B->full[told % kStages]);
-            ++told;
-          }
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          if (g > 0) arrive_warp(&B->full[(g - 1) % kStages]);
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      for (; told < g; ++told) arrive_warp(&B->full[told % kStages]);
+      if (g > 0) arrive_warp(&B->full[(g - 1) % kStages]);
     }
   } else {
     // ---------------------------------------------------------- epilogue
-    const int q = warp & 3;           // TMEM lane quarter of this warp
-    const int half = (warp - 6) >> 2;  // takes the 16-column chunks of this parity
-    int i = 0;
-    for (int w = blockIdx.x; w < total; w += G, ++i) {
-      const Item it = item_at(P, *B, w);
-      const int acc = i & 1;
+    // A thread has one output row; two warps share a lane quarter, 32 columns in turn.
+    const int q = warp & 3;                   // TMEM lane quarter of this warp
+    const int half = (warp - kWarpEpi) >> 2;
+    const int r = q * 32 + lane;
+    constexpr int kOut = SWIGLU ? 2 : 1;      // weight rows per result
+    constexpr int kWords = 32 / kOut * sizeof(T) / 4;  // of a row's 32 columns
+    uint4* stage_out = reinterpret_cast<uint4*>(smem + Sh::kOut) + 256 * (warp - kWarpEpi);
+    for (int i = 0; i < n_items; ++i) {
+      const Item it = item_at<Sh>(P, *B, i);
+      const int acc = i & 1, p = it.row0 + r;
+      const bool live = r < it.rows;
+      const float gate = P.gate && live && p < P.n_pairs ? __ldg(P.pair_gate + p) : 1.f;
       if (!wait_warp(B, &B->d_full[acc], (i >> 1) & 1, P, 6)) break;
-      tc_fence_after();
-      const uint32_t base = tmem + static_cast<uint32_t>(acc * kAcc) + (static_cast<uint32_t>(q * 32) << 16);
-      const int wr = it.m * kBM + q * 32 + lane;
-      for (int c0 = 16 * half; c0 < it.rows; c0 += 32) {
-        float gate_l = 1.f;
-        if (P.gate) {
-          const int c = c0 + (lane & 15), p = it.row0 + c;
-          if (c < it.rows && p < P.n_pairs) gate_l = __ldg(P.pair_gate + p);
+      if (q * 32 < it.rows) {
+        tc_fence_after();
+        const uint32_t base = tmem + static_cast<uint32_t>(acc * kAcc) + (static_cast<uint32_t>(q * 32) << 16);
+        const int n = min(Sh::kBN, P.w_rows - it.n0);
+        for (int c0 = 32 * half; c0 < n; c0 += 64) {
+          float v[32];
+          uint32_t words[kWords];
+          tmem_ld16(base + c0, v);
+          if (c0 + 16 < n) tmem_ld16(base + c0 + 16, v + 16);
+          results16<T, SWIGLU>(v, gate, words);
+          results16<T, SWIGLU>(v + 16, gate, words + kWords / 2);
+          T* dst = static_cast<T*>(P.out) + (it.n0 + c0) / kOut;  // the chunk's place in row 0
+          const int valid = c0 + 16 < n ? kWords : kWords / 2;
+          if (kWords >= 16 && P.vec >= 16)
+            store_staged<T, kWords>(stage_out, words, dst + (it.row0 + q * 32) * P.ld, P.ld, it.rows - q * 32, valid);
+          else if (live)
+            store_row<T, kWords>(dst + p * P.ld, words, valid, P.vec);
+          __syncwarp();
         }
-        __syncwarp();
-        float v[16];
-        tmem_ld16(base + c0, v);
-        store16<T, SWIGLU>(P, v, wr, static_cast<long long>(it.row0) + c0, it.rows - c0, gate_l);
+        tc_fence_before();
       }
-      tc_fence_before();
       mbar_arrive(&B->d_empty[acc]);
     }
   }
@@ -625,16 +714,17 @@ bool map_codes(CUtensorMap* m, const uint8_t* base, int row_bytes, int rows, int
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T>
+template <typename Sh, typename T>
 const void* kernel_of(bool swiglu) {
-  return swiglu ? reinterpret_cast<const void*>(mx4_product_kernel<T, true>)
-                : reinterpret_cast<const void*>(mx4_product_kernel<T, false>);
+  return swiglu ? reinterpret_cast<const void*>(mx4_product_kernel<Sh, T, true>)
+                : reinterpret_cast<const void*>(mx4_product_kernel<Sh, T, false>);
 }
 
+template <typename Sh>
 const void* kernel_of(int type, bool swiglu) {
-  return type == MOE_TYPE_BF16   ? kernel_of<__nv_bfloat16>(swiglu)
-         : type == MOE_TYPE_FP16 ? kernel_of<__half>(swiglu)
-                                 : kernel_of<float>(swiglu);
+  return type == MOE_TYPE_BF16   ? kernel_of<Sh, __nv_bfloat16>(swiglu)
+         : type == MOE_TYPE_FP16 ? kernel_of<Sh, __half>(swiglu)
+                                 : kernel_of<Sh, float>(swiglu);
 }
 
 }  // namespace
@@ -643,8 +733,11 @@ cudaError_t mx4_product_init(const Ctx& ctx) {
   (void)ctx;
   for (int type = MOE_TYPE_BF16; type <= MOE_TYPE_FP32; ++type)
     for (int swiglu = 0; swiglu < 2; ++swiglu) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel_of(type, swiglu != 0),
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      cudaError_t e = cudaFuncSetAttribute(kernel_of<Wide>(type, swiglu != 0),
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, Wide::kSmem);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel_of<Narrow>(type, swiglu != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Narrow::kSmem);
       if (e != cudaSuccess) return e;
     }
   return cudaSuccess;
@@ -662,8 +755,7 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   P.n_slots = a.w.n_slots;
   P.K = a.w.cols;
   P.pitch = mx4_pitch(a.w.cols);
-  P.m_tiles = (a.w.rows + kBM - 1) / kBM;
-  P.grouped = a.g != nullptr;
+    P.grouped = a.g != nullptr;
   long long groups = 1, rows = a.x_rows;  // at most
   if (a.g != nullptr) {
     P.n_uniq = a.g->n_uniq;
@@ -680,18 +772,25 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   P.shared_slot = a.shared_slot;
   P.gather = a.gather;
   P.gate = a.gate;
-  P.pack = a.ld % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
+  const size_t mix = reinterpret_cast<uintptr_t>(a.out) | (a.ld * (a.out_type == MOE_TYPE_FP32 ? 4 : 2));
+  P.vec = mix % 32 == 0 ? 32 : mix % 16 == 0 ? 16 : 0;
   P.out = a.out;
   P.ld = static_cast<long long>(a.ld);
   P.status = ctx.d_status;
   P.timeout_ns = ctx.timeout_ns;
-  const long long items = (rows / kBN + groups) * P.m_tiles;
+  // Groups of at most 64 rows (no group has more rows than there are tokens,
+  // unless a token names an expert twice): small stages, and more of them in
+  // flight.
+  const bool narrow = (a.g != nullptr ? a.g->T : a.x_rows) <= Narrow::kBM;
+  const int bm = narrow ? Narrow::kBM : Wide::kBM, bn = narrow ? Narrow::kBN : Wide::kBN;
+  P.w_tiles = (a.w.rows + bn - 1) / bn;
+  const long long items = (rows / bm + groups) * P.w_tiles;
   if (items > 0x7fffffff) return cudaErrorNotSupported;
 
   const int row_b = a.w.cols / 2;
   CUtensorMap tw, txa, txb;
   const size_t stride = a.w.n_slots > 1 ? a.w.code_stride : static_cast<size_t>(a.w.rows) * row_b;
-  if (!map_codes(&tw, a.w.codes, row_b, a.w.rows, a.w.n_slots, stride, 3, kBM)) return cudaErrorInvalidValue;
+  if (!map_codes(&tw, a.w.codes, row_b, a.w.rows, a.w.n_slots, stride, 3, bn)) return cudaErrorInvalidValue;
   if (a.gather)
     txa = txb = tw;  // not used: the x rows are copied one by one
   else if (!map_codes(&txa, a.x_codes, row_b, a.x_rows, 1, 0, 2, kBoxA) ||
@@ -701,7 +800,7 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items < ctx.num_sms ? items : ctx.num_sms));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = narrow ? Narrow::kSmem : Wide::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -709,7 +808,8 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   void* args[] = {&tw, &txa, &txb, &P};
-  return cudaLaunchKernelExC(&cfg, kernel_of(a.out_type, a.swiglu), args);
+  return cudaLaunchKernelExC(
+      &cfg, narrow ? kernel_of<Narrow>(a.out_type, a.swiglu) : kernel_of<Wide>(a.out_type, a.swiglu), args);
 }
 
 }  // namespace moe
