@@ -37,7 +37,7 @@ namespace moe {
 namespace {
 
 // warps by role
-constexpr int kWarpScales = 2, kScaleWarps = 3;
+constexpr int kWarpScales = 2, kScaleParts = 3, kScaleWarps = 2 * kScaleParts;
 constexpr int kWarpEpi = kWarpScales + kScaleWarps, kEpiWarps = 8;
 constexpr int kWarpGather = kWarpEpi + kEpiWarps, kGatherWarps = 4;
 constexpr int kThreads = 32 * (kWarpGather + kGatherWarps);
@@ -51,7 +51,8 @@ constexpr int kMaxStages = 7;
 
 // The groups' row tiles, laid end to end: group i's first is prefix[i].
 struct Table {
-  uint64_t full[kMaxStages];   // TMA (tx), scale warps, gather warps: a stage is complete
+  uint64_t full[kMaxStages];   // TMA (tx), scale warps: a stage is complete
+  uint64_t x_full[kMaxStages]; // gather threads (count 128), waited on by the x rows' scale warp
   uint64_t empty[kMaxStages];  // MMA commit: codes and scales read
   uint64_t d_full[2];          // MMA commit: accumulator complete
   uint64_t d_empty[2];         // epilogue (count 256)
@@ -127,12 +128,12 @@ __device__ __forceinline__ bool wait_bar(Table* B, uint64_t* bar, uint32_t parit
   return false;
 }
 
-// Lane 0 waits; every lane takes the same path afterwards.
+// The same for a whole warp, every lane taking the same path afterwards.
 __device__ __forceinline__ bool wait_warp(Table* B, uint64_t* bar, uint32_t parity, const Params& P, int where) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   int ok = 1;
   if ((threadIdx.x & 31) == 0) ok = wait_bar(B, bar, parity, P, where) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  return ok != 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
 template <typename S>
@@ -223,18 +224,24 @@ __device__ __forceinline__ Item item_at(const Params& P, const Table& S, int i) 
   return {v.x, v.y, v.z, v.w};
 }
 
-// x row of output row p; out-of-range tokens are clamped (and reported by the
-// scale threads).
+// x row of output row p as the grouping names it; clamp_row makes it one of
+// x's (out-of-range tokens are reported by the scale warps). The two are apart
+// so that a load's latency is not waited for where it is issued.
 __device__ __forceinline__ int source_row(const Params& P, int p) {
-  if (!P.gather) return p;
-  const int t = p < P.n_pairs ? __ldg(P.pair_token + p) : p - P.n_pairs;
-  return min(max(t, 0), P.x_rows - 1);
+  return !P.gather ? p : p < P.n_pairs ? __ldg(P.pair_token + p) : p - P.n_pairs;
 }
+__device__ __forceinline__ int clamp_row(const Params& P, int t) { return min(max(t, 0), P.x_rows - 1); }
 
 // 16 bytes to shared memory without passing through registers; zeros where
 // `live` is false.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+// One arrival on `bar` (counted in its initial number) once every copy16 this
+// thread has issued is complete.
+__device__ __forceinline__ void copy16_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // 32 rows of 16 bytes, to four 32-bit columns of every lane quarter.
@@ -308,8 +315,6 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <>
 __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ float narrow<float>(float v) { return v; }
 
 // 1 / x of x in [1, infinity], within a step (0 above 2^126).
 __device__ __forceinline__ float fast_rcp(float x) {
@@ -421,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&B->full[i], 1 + kScaleWarps + (P.gather ? kGatherWarps : 0));
+      mbar_init(&B->full[i], 1 + kScaleParts);
+      mbar_init(&B->x_full[i], kGatherThreads);
       mbar_init(&B->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -487,17 +493,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sa0 = scale_desc(smem + Sh::kSfX), sb0 = scale_desc(smem + Sh::kSfW);
     int st = 0;
     uint32_t ph = 0;
-    bool ok = true;
+    bool ok = true, ready = false;
     for (int i = 0; i < n_items && ok; ++i) {
       const Item it = item_at<Sh>(P, *B, i);
       const int n = min(Sh::kBN, P.w_rows - it.n0);
       const uint32_t id0 = instr_desc_mxf4(n, 0), id1 = instr_desc_mxf4(n, 1);
       const int acc = i & 1;
-      if (i >= 2 && !wait_bar(B, &B->d_empty[acc], ((i >> 1) - 1) & 1, P, 2)) break;
+      if (i >= 2 && !wait_warp(B, &B->d_empty[acc], ((i >> 1) - 1) & 1, P, 2)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * kAcc);
       for (int k = 0; k < n_k; ++k) {
-        if (!wait_bar(B, &B->full[st], ph, P, 3)) {
+        if (!ready && !wait_warp(B, &B->full[st], ph, P, 3)) {
           ok = false;
           break;
         }
@@ -527,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           st = 0;
           ph ^= 1;
         }
+        ready = __all_sync(0xffffffffu, mbar_test(&B->full[st], ph));  // the next stage's, while these MMAs run
       }
     }
     // everything issued above completes before the tensor memory is freed
@@ -540,40 +547,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Lane l loads the scales of rows l, l + 32, l + 64, l + 96 for 16 K blocks
     // (two stages) and stores, for each piece of 4 blocks, the four rows' words
     // side by side.
-    const int part = warp - kWarpScales;
-    const int blocks = P.K / kBlock;
-    int g = 0;
-    bool ok = true;
-    for (int i = 0; i < n_items && ok; ++i) {
+    // Two warps per part take turns, 16 blocks each. Loads run one turn ahead,
+    // over the item's end too, and the tokens one item ahead.
+    const int part = (warp - kWarpScales) % kScaleParts, turn = (warp - kWarpScales) / kScaleParts;
+    const int blocks = P.K / kBlock, n_pairs_k = (n_k + 1) / 2;
+    int tok[4];  // x rows of the item that comes next (-1: none)
+    auto tokens_of = [&](int i) {
+      if (part > 0 || i >= n_items) return;
       const Item it = item_at<Sh>(P, *B, i);
-      const bool any = part <= kPieces;
-      const uint8_t* rows[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        rows[j] = nullptr;
         const int r = lane + 32 * j;
-        if (part > 0) {
-          const int wr = it.n0 + 128 * (part - 1) + r;
-          if (any && wr < P.w_rows)
-            rows[j] = P.ws + static_cast<size_t>(it.slot) * P.ws_stride + static_cast<size_t>(wr) * P.pitch;
-        } else if (r < it.rows) {
-          const int p = it.row0 + r;
-          if (P.gather && it.n0 == 0 && p < P.n_pairs &&
-              static_cast<unsigned>(__ldg(P.pair_token + p)) >= static_cast<unsigned>(P.x_rows))
-            report(P.status, kDevBadExpert, p);
-          rows[j] = P.xs + static_cast<size_t>(source_row(P, p)) * P.pitch;
+        tok[j] = r < it.rows ? source_row(P, it.row0 + r) : -1;
+      }
+    };
+    const uint8_t* rows[4];
+    auto rows_of = [&](int i) {
+      const Item it = item_at<Sh>(P, *B, i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = lane + 32 * j, wr = it.n0 + 128 * (part - 1) + r;
+        rows[j] = nullptr;
+        if (part == 0 && r < it.rows) {
+          if (it.n0 == 0 && static_cast<unsigned>(tok[j]) >= static_cast<unsigned>(P.x_rows))
+            report(P.status, kDevBadExpert, it.row0 + r);
+          rows[j] = P.xs + static_cast<size_t>(clamp_row(P, tok[j])) * P.pitch;
+        } else if (part > 0 && part <= kPieces && wr < P.w_rows) {
+          rows[j] = P.ws + static_cast<size_t>(it.slot) * P.ws_stride + static_cast<size_t>(wr) * P.pitch;
         }
       }
-      uint4 next[4];
+    };
+    uint4 next[4];
+    auto load = [&](int pair) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) next[j] = rows[j] != nullptr ? load_scales(rows[j], 0, blocks) : make_uint4(0, 0, 0, 0);
-      for (int pair = 0; 2 * pair < n_k && ok; ++pair) {
-        uint4 cur[4];
+      for (int j = 0; j < 4; ++j)
+        next[j] = rows[j] != nullptr ? load_scales(rows[j], pair, blocks) : make_uint4(0, 0, 0, 0);
+    };
+    // this warp's turns: every second one of the items' n_pairs_k each
+    const int stride = n_pairs_k >= 2 ? 1 : 2;  // items from one that it meets to the next
+    int i = turn / n_pairs_k, pair = turn % n_pairs_k;
+    bool ok = true;
+    if (i < n_items) {
+      tokens_of(i);
+      rows_of(i);
+      load(pair);
+      tokens_of(i + stride);
+    }
+    while (i < n_items && ok) {
+      uint4 cur[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          cur[j] = next[j];
-          if (rows[j] != nullptr && 2 * pair + 2 < n_k) next[j] = load_scales(rows[j], pair + 1, blocks);
-        }
+      for (int j = 0; j < 4; ++j) cur[j] = next[j];
+      int i2 = i, pair2 = pair + 2;
+      while (pair2 >= n_pairs_k) {
+        pair2 -= n_pairs_k;
+        ++i2;
+      }
+      if (i2 < n_items) {
+        if (i2 != i) rows_of(i2);
+        load(pair2);
+        if (i2 != i) tokens_of(i2 + stride);
+      }
+      {
+        int g = i * n_k + 2 * pair;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (2 * pair + s >= n_k) break;
@@ -582,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (any) {
+          if (part <= kPieces) {
             uint8_t* stage = smem + st * Sh::kStage;
             uint4* p0 = reinterpret_cast<uint4*>(stage + (part == 0 ? Sh::kSfX : Sh::kSfW + 512 * (part - 1))) + lane;
             uint4* p1 = p0 + (part == 0 ? 512 : 512 * kPieces) / 16;
@@ -594,10 +629,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               *p1 = make_uint4(cur[0].w, cur[1].w, cur[2].w, cur[3].w);
             }
           }
-          arrive_warp(&B->full[st]);  // the stores above are read by the asynchronous scale copies
+          // the gathered rows' writes are announced with this warp's own
+          if (part == 0 && P.gather && !wait_warp(B, &B->x_full[st], (g / kStages) & 1, P, 7)) {
+            ok = false;
+            break;
+          }
+          arrive_warp(&B->full[st]);  // the stores are read by the asynchronous scale copies
           ++g;
         }
       }
+      i = i2;
+      pair = pair2;
     }
   } else if (warp >= kWarpGather) {
     // ---------------------------------------------------------- gathered x rows
@@ -609,14 +651,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row_b = P.K / 2;
       int g = 0;
       bool ok = true;
-      for (int i = 0; i < n_items && ok; ++i) {
+      int src[kGatherRows], ahead[kGatherRows];  // this item's rows, the next one's
+      auto rows_of = [&](int i) {
+        if (i >= n_items) return;
         const Item it = item_at<Sh>(P, *B, i);
-        int src[kGatherRows];
 #pragma unroll
         for (int j = 0; j < kGatherRows; ++j) {
           const int r = r0 + 16 * j;
-          src[j] = r < it.rows ? source_row(P, it.row0 + r) : 0;
+          ahead[j] = r < it.rows ? source_row(P, it.row0 + r) : 0;
         }
+      };
+      rows_of(0);
+      for (int i = 0; i < n_items && ok; ++i) {
+        const Item it = item_at<Sh>(P, *B, i);
+#pragma unroll
+        for (int j = 0; j < kGatherRows; ++j) src[j] = clamp_row(P, ahead[j]);
+        rows_of(i + 1);
         for (int k = 0; k < n_k; ++k, ++g) {
           const int st = g % kStages;
           if (g >= kStages && !wait_warp(B, &B->empty[st], ((g / kStages) - 1) & 1, P, 8)) {
@@ -631,14 +681,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < kGatherRows; ++j)
             if (r0 + 16 * j < it.rows)
               copy16(dst + j * 16 * 128, base + static_cast<size_t>(src[j]) * row_b, live);
-          // stage g - 1 is announced once this one is on its way
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          if (g > 0) arrive_warp(&B->full[(g - 1) % kStages]);
+          copy16_arrive(&B->x_full[st]);
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (g > 0) arrive_warp(&B->full[(g - 1) % kStages]);
+      asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight when the CTA exits
     }
   } else {
     // ---------------------------------------------------------- epilogue
