@@ -225,10 +225,18 @@ __device__ __forceinline__ Item item_at(const Params& P, const Table& S, int i) 
 }
 
 // x row of output row p as the grouping names it; clamp_row makes it one of
-// x's (out-of-range tokens are reported by the scale warps). The two are apart
-// so that a load's latency is not waited for where it is issued.
+// x's (out-of-range tokens are reported by the scale warps). The two are apart,
+// and the load is a predicated one, so that its latency is not waited for where
+// it is issued.
 __device__ __forceinline__ int source_row(const Params& P, int p) {
-  return !P.gather ? p : p < P.n_pairs ? __ldg(P.pair_token + p) : p - P.n_pairs;
+  int t = P.gather && p >= P.n_pairs ? p - P.n_pairs : p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "@p ld.global.nc.b32 %0, [%1];\n\t}"
+      : "+r"(t)
+      : "l"(P.pair_token + p), "r"(P.gather && p < P.n_pairs ? 1 : 0));
+  return t;
 }
 __device__ __forceinline__ int clamp_row(const Params& P, int t) { return min(max(t, 0), P.x_rows - 1); }
 
@@ -293,20 +301,11 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// The scale bytes of blocks 16 pair .. 16 pair + 15 of one row as four words
-// (blocks past the row's end read as 0).
-__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pair, int blocks) {
-  uint4 v = __ldg(reinterpret_cast<const uint4*>(row) + pair);
-  const int left = blocks - 16 * pair;  // bytes that are scales
-  if (left < 16) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = min(max(left - 4 * i, 0), 4);
-      w[i] = n == 4 ? w[i] : w[i] & ((1u << (8 * n)) - 1u);
-    }
-  }
-  return v;
+// The bytes of four K blocks (word i of 16) that are scales of a row with
+// `left` blocks from the first word's on; the others 0.
+__device__ __forceinline__ uint32_t mask_scales(uint32_t w, int i, int left) {
+  const int n = min(max(left - 4 * i, 0), 4);
+  return n == 4 ? w : w & ((1u << (8 * n)) - 1u);
 }
 
 template <typename T>
@@ -551,37 +550,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     // over the item's end too, and the tokens one item ahead.
     const int part = (warp - kWarpScales) % kScaleParts, turn = (warp - kWarpScales) / kScaleParts;
     const int blocks = P.K / kBlock, n_pairs_k = (n_k + 1) / 2;
-    int tok[4];  // x rows of the item that comes next (-1: none)
+    // Rows past the item's end take its last row: nobody reads their results.
+    int tok[4];  // x rows of the item that comes next
     auto tokens_of = [&](int i) {
       if (part > 0 || i >= n_items) return;
       const Item it = item_at<Sh>(P, *B, i);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = lane + 32 * j;
-        tok[j] = r < it.rows ? source_row(P, it.row0 + r) : -1;
-      }
+      for (int j = 0; j < 4; ++j) tok[j] = source_row(P, it.row0 + min(lane + 32 * j, it.rows - 1));
     };
     const uint8_t* rows[4];
     auto rows_of = [&](int i) {
       const Item it = item_at<Sh>(P, *B, i);
+      if (part == 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = lane + 32 * j, wr = it.n0 + 128 * (part - 1) + r;
-        rows[j] = nullptr;
-        if (part == 0 && r < it.rows) {
-          if (it.n0 == 0 && static_cast<unsigned>(tok[j]) >= static_cast<unsigned>(P.x_rows))
+        for (int j = 0; j < 4; ++j) {
+          const int r = lane + 32 * j;
+          if (it.n0 == 0 && r < it.rows && static_cast<unsigned>(tok[j]) >= static_cast<unsigned>(P.x_rows))
             report(P.status, kDevBadExpert, it.row0 + r);
           rows[j] = P.xs + static_cast<size_t>(clamp_row(P, tok[j])) * P.pitch;
-        } else if (part > 0 && part <= kPieces && wr < P.w_rows) {
-          rows[j] = P.ws + static_cast<size_t>(it.slot) * P.ws_stride + static_cast<size_t>(wr) * P.pitch;
         }
+      } else {
+        const uint8_t* base = P.ws + static_cast<size_t>(it.slot) * P.ws_stride;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          rows[j] = base + static_cast<size_t>(min(it.n0 + 128 * (part - 1) + lane + 32 * j, P.w_rows - 1)) * P.pitch;
       }
     };
     uint4 next[4];
     auto load = [&](int pair) {
+      if (part > kPieces) return;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        next[j] = rows[j] != nullptr ? load_scales(rows[j], pair, blocks) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 4; ++j) next[j] = __ldg(reinterpret_cast<const uint4*>(rows[j]) + pair);
     };
     // this warp's turns: every second one of the items' n_pairs_k each
     const int stride = n_pairs_k >= 2 ? 1 : 2;  // items from one that it meets to the next
@@ -597,6 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint4 cur[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) cur[j] = next[j];
+      const int left = blocks - 16 * pair;
+      if (left < 16) {  // the row's end: bytes past it are not scales
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          cur[j] = make_uint4(mask_scales(cur[j].x, 0, left), mask_scales(cur[j].y, 1, left),
+                              mask_scales(cur[j].z, 2, left), mask_scales(cur[j].w, 3, left));
+      }
       int i2 = i, pair2 = pair + 2;
       while (pair2 >= n_pairs_k) {
         pair2 -= n_pairs_k;
@@ -656,10 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i >= n_items) return;
         const Item it = item_at<Sh>(P, *B, i);
 #pragma unroll
-        for (int j = 0; j < kGatherRows; ++j) {
-          const int r = r0 + 16 * j;
-          ahead[j] = r < it.rows ? source_row(P, it.row0 + r) : 0;
-        }
+        for (int j = 0; j < kGatherRows; ++j) ahead[j] = source_row(P, it.row0 + min(r0 + 16 * j, it.rows - 1));
       };
       rows_of(0);
       for (int i = 0; i < n_items && ok; ++i) {
