@@ -253,8 +253,13 @@ __device__ __forceinline__ void copy16_arrive(uint64_t* bar) {
 }
 
 // 32 rows of 16 bytes, to four 32-bit columns of every lane quarter.
-__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t desc, uint32_t desc_hi) {
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\t"
+      "mov.b64 d, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+      "r"(desc), "r"(desc_hi)
+      : "memory");
 }
 
 // Descriptor of such a piece: no swizzle, cores of 8 rows x 16 bytes, 128 bytes apart.
@@ -274,14 +279,17 @@ __device__ __forceinline__ uint32_t instr_desc_mxf4(int n, uint32_t half) {
          (static_cast<uint32_t>(128 >> 7) << 27) | (half << 30);
 }
 
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                            uint32_t sfb, uint32_t acc) {
+// a, b: low words of the operands' descriptors, whose high words are the same.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                            uint32_t sfa, uint32_t sfb, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %4, [%6], [%7], p;\n\t}" ::"r"(
           d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
       : "memory");
 }
 
@@ -489,43 +497,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp walks the loop and one lane issues: the operands then stay
     // in uniform registers, and a stage costs the issuer less than its MMAs take.
     const uint64_t da0 = smem_desc(smem + Sh::kX), db0 = smem_desc(smem + Sh::kW);
-    const uint64_t sa0 = scale_desc(smem + Sh::kSfX), sb0 = scale_desc(smem + Sh::kSfW);
+    const uint32_t hi = static_cast<uint32_t>(da0 >> 32);
+    const uint32_t a0 = static_cast<uint32_t>(da0), b0 = static_cast<uint32_t>(db0);
+    const uint64_t dsx = scale_desc(smem + Sh::kSfX), dsw = scale_desc(smem + Sh::kSfW);
+    const uint32_t hs = static_cast<uint32_t>(dsx >> 32);
+    const uint32_t sx = static_cast<uint32_t>(dsx), sw = static_cast<uint32_t>(dsw);
     int st = 0;
     uint32_t ph = 0;
     bool ok = true, ready = false;
     for (int i = 0; i < n_items && ok; ++i) {
-      const Item it = item_at<Sh>(P, *B, i);
-      const int n = min(Sh::kBN, P.w_rows - it.n0);
+      const int n = min(Sh::kBN, P.w_rows - item_at<Sh>(P, *B, i).n0);
       const uint32_t id0 = instr_desc_mxf4(n, 0), id1 = instr_desc_mxf4(n, 1);
       const int acc = i & 1;
       if (i >= 2 && !wait_warp(B, &B->d_empty[acc], ((i >> 1) - 1) & 1, P, 2)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * kAcc);
-      for (int k = 0; k < n_k; ++k) {
+      int left = P.K;  // K values
+      for (int k = 0; k < n_k; ++k, left -= kBK) {
         if (!ready && !wait_warp(B, &B->full[st], ph, P, 3)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint64_t off = static_cast<uint64_t>(st * (Sh::kStage >> 4));
+        const uint32_t off = static_cast<uint32_t>(st * (Sh::kStage >> 4));
         const uint32_t sf = tmem + static_cast<uint32_t>(2 * kAcc + st * Sh::kSfCols);
-        const int steps = P.K - k * kBK;  // K values left
         if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (h == 1 && steps <= 128) break;
-            tc_copy_scales(sf + 4 * h, sa0 + off + 32 * h);
+            tc_copy_scales(sf + 4 * h, sx + off + 32 * h, hs);
 #pragma unroll
             for (int j = 0; j < kPieces; ++j)
-              tc_copy_scales(sf + 8 + 4 * (kPieces * h + j), sb0 + off + 32 * (kPieces * h + j));
+              tc_copy_scales(sf + 8 + 4 * (kPieces * h + j), sw + off + 32 * (kPieces * h + j), hs);
           }
 #pragma unroll
           for (int s = 0; s < 4; ++s)  // K = 64 per MMA: 32 bytes of a row
-            if (64 * s < steps)
-              tc_mma_mxf4(d_tmem, da0 + off + 2 * s, db0 + off + 2 * s, (s & 1) ? id1 : id0, sf + 4 * (s >> 1),
+            if (s == 0 || 64 * s < left)
+              tc_mma_mxf4(d_tmem, a0 + off + 2 * s, b0 + off + 2 * s, hi, (s & 1) ? id1 : id0, sf + 4 * (s >> 1),
                           sf + 8 + 4 * kPieces * (s >> 1), (k > 0 || s > 0) ? 1u : 0u);
           tc_commit(&B->empty[st]);
-          if (k == n_k - 1) tc_commit(&B->d_full[acc]);
+          if (left <= kBK) tc_commit(&B->d_full[acc]);
         }
         __syncwarp();
         if (++st == kStages) {
