@@ -17,6 +17,10 @@
 // thread takes 8 values of a row (one 16-byte load of 16-bit values, two of
 // fp32), a block's maximum takes two shuffles among its four lanes, the codes
 // leave as one 4-byte word per thread.
+#include <string.h>
+
+#include <type_traits>
+
 #include "moe_internal.cuh"
 #include "ptx.cuh"
 
@@ -26,42 +30,95 @@ namespace {
 constexpr int kQThreads = 256;
 constexpr int kQUnits = 4;  // units of 8 values per thread: their loads are in flight together
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, float* v);
+// Eight values as fp32 and the largest magnitude among them; NaN if one is.
+template <typename T>
+struct Values;
 
 template <>
-__device__ __forceinline__ void load8<float, true>(const float* p, float* v) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16, true>(const __nv_bfloat16* p, float* v) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+struct Values<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
-}
-template <>
-__device__ __forceinline__ void load8<__half, true>(const __half* p, float* v) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  __device__ __forceinline__ void load_each(const float* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+    for (int i = 0; i < 8; ++i) v[i] = __ldg(p + i);
   }
-}
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, float* v) {
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  }
+  __device__ __forceinline__ float get(int i) const { return v[i]; }
+  __device__ __forceinline__ float top() const {
+    float m = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = nan_max(m, fabsf(v[i]));
+    m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return nan_max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  }
+  __device__ __forceinline__ static float nan_max(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+  }
+};
+
+// 16-bit types stay packed in pairs: magnitudes and their maximum two at a time.
+template <typename T2>
+struct Pairs {
+  uint32_t w[4];
+  template <typename T>
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  }
+  template <typename T>
+  __device__ __forceinline__ void load_each(const T* p) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __ldg(q + 2 * i) | static_cast<uint32_t>(__ldg(q + 2 * i + 1)) << 16;
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+  __device__ __forceinline__ static T2 as2(uint32_t x) { return *reinterpret_cast<const T2*>(&x); }
+  __device__ __forceinline__ static uint32_t bits(T2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+  __device__ __forceinline__ uint32_t top2() const {
+    T2 m = __hmax2_nan(as2(w[0] & 0x7fff7fffu), as2(w[1] & 0x7fff7fffu));
+    m = __hmax2_nan(m, __hmax2_nan(as2(w[2] & 0x7fff7fffu), as2(w[3] & 0x7fff7fffu)));
+    m = __hmax2_nan(m, as2(__shfl_xor_sync(0xffffffffu, bits(m), 1)));
+    m = __hmax2_nan(m, as2(__shfl_xor_sync(0xffffffffu, bits(m), 2)));
+    return bits(m);
+  }
+};
+template <>
+struct Values<__nv_bfloat16> : Pairs<__nv_bfloat162> {
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float((i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ float top() const {
+    const uint32_t m = top2();
+    return Values<float>::nan_max(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
+template <>
+struct Values<__half> : Pairs<__half2> {
+  __device__ __forceinline__ float get(int i) const {
+    const __half2 h = as2(w[i / 2]);
+    return (i & 1) ? __high2float(h) : __low2float(h);
+  }
+  __device__ __forceinline__ float top() const {
+    const __half2 m = as2(top2());
+    return Values<float>::nan_max(__low2float(m), __high2float(m));
+  }
+};
+
+// a * b on two fp32 lanes at once.
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
 }
 
 // Eight values to eight codes, value 0 in the lowest four bits.
@@ -97,22 +154,22 @@ __device__ __forceinline__ void levels8(uint32_t c, float* v) {
   }
 }
 
-// Row and unit (8 values) of a flat unit index, from the index of the CTA's
-// first unit: one 64-bit division per CTA, then a multiplication by
-// ceil(2^32 / upr), exact while n * upr < 2^32 (cols <= kMx4MaxCols: n < upr +
-// 1024 <= 9216).
+// Row (from the CTA's first) and unit (of 8 values) of the CTA's local-th
+// unit: one 64-bit division per CTA, then a multiplication by ceil(2^32 / upr),
+// exact while n * upr < 2^32 (cols <= kMx4MaxCols: n < upr + 1024 <= 9216).
 struct RowOf {
   long long row0;
-  uint32_t rem0, upr, magic;
-  __device__ RowOf(long long u0, uint32_t upr_, uint32_t magic_) : upr(upr_), magic(magic_) {
+  uint32_t rem0, upr, magic, count;
+  __device__ RowOf(long long units, uint32_t upr_, uint32_t magic_) : upr(upr_), magic(magic_) {
+    const long long u0 = static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits);
     row0 = u0 / upr;
     rem0 = static_cast<uint32_t>(u0 - row0 * upr);
+    count = static_cast<uint32_t>(min(units - u0, static_cast<long long>(kQThreads * kQUnits)));
   }
-  __device__ __forceinline__ void at(uint32_t local, long long& row, uint32_t& unit) const {
+  __device__ __forceinline__ void at(uint32_t local, uint32_t& row, uint32_t& unit) const {
     const uint32_t n = rem0 + local;
-    const uint32_t q = __umulhi(n, magic);
-    row = row0 + q;
-    unit = n - q * upr;
+    row = __umulhi(n, magic);
+    unit = n - row * upr;
   }
 };
 
@@ -121,99 +178,122 @@ __global__ void __launch_bounds__(kQThreads) mx4_quantize_kernel(const T* __rest
                                                                  long long units, uint32_t upr, uint32_t magic,
                                                                  int pitch, uint8_t* __restrict__ codes,
                                                                  uint8_t* __restrict__ scales) {
-  const long long u0 = static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits);
-  const RowOf rows(u0, upr, magic);
+  const RowOf rows(units, upr, magic);
+  x += rows.row0 * ld;
+  scales += rows.row0 * pitch;
+  uint32_t* out = reinterpret_cast<uint32_t*>(codes) + static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits);
   grid_dep_launch();  // a product that follows sets up meanwhile; it waits for this grid's end
   grid_dep_wait();
-  float v[kQUnits][8];
-  long long row[kQUnits];
-  uint32_t unit[kQUnits];
+  Values<T> v[kQUnits];
 #pragma unroll
   for (int i = 0; i < kQUnits; ++i) {
     const uint32_t local = i * kQThreads + threadIdx.x;
-    rows.at(local, row[i], unit[i]);
-    if (u0 + local < units) {
-      load8<T, VEC>(x + row[i] * ld + unit[i] * 8, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
+    uint32_t row, unit;
+    rows.at(local, row, unit);
+    const T* p = x + row * ld + unit * 8;
+    if (local >= rows.count)
+      v[i].zero();
+    else if (VEC)
+      v[i].load(p);
+    else
+      v[i].load_each(p);
   }
 #pragma unroll
   for (int i = 0; i < kQUnits; ++i) {
     const uint32_t local = i * kQThreads + threadIdx.x;
-    // magnitudes compare as integers; infinities and NaN come out on top
-    uint32_t m = 0;
+    uint32_t row, unit;
+    rows.at(local, row, unit);
+    const float m = v[i].top();
+    const bool bad = !(m < INFINITY);
+    const uint32_t e = max(static_cast<int>(__float_as_uint(m) >> 23) - 2, 0);
+    const float inv = __uint_as_float((254u - e) << 23);
+    float s[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const bool bad = m >= 0x7f800000u;
-    const int e = max(static_cast<int>(m >> 23) - 2, 0);
-    const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-    const uint32_t c = bad ? 0u : codes8(v[i]);
-    if (u0 + local >= units) continue;
-    *reinterpret_cast<uint32_t*>(codes + (u0 + local) * 4) = c;
-    if ((unit[i] & 3) == 0) {
-      uint8_t* s = scales + row[i] * pitch + (unit[i] >> 2);
-      *s = bad ? 255 : static_cast<uint8_t>(e);
-      if (unit[i] + 4 == upr)  // the row's last block also clears the padding
-        for (int b = upr / 4; b < pitch; ++b) scales[row[i] * pitch + b] = 0;
+    for (int j = 0; j < 4; ++j) {
+      const float2 q = fmul2(make_float2(v[i].get(2 * j), v[i].get(2 * j + 1)), make_float2(inv, inv));
+      s[2 * j] = q.x, s[2 * j + 1] = q.y;
+    }
+    const uint32_t c = codes8(s);
+    if (local >= rows.count) continue;
+    out[local] = bad ? 0u : c;
+    if ((unit & 3) == 0) {
+      uint8_t* b = scales + row * pitch + (unit >> 2);
+      *b = bad ? 255 : static_cast<uint8_t>(e);
+      if (unit + 4 == upr)  // the row's last block also clears the padding
+        for (int k = upr / 4; k < pitch; ++k) *++b = 0;
     }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+// Eight fp32 results to p in T.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* p, const float* v) {
+  constexpr int kW = 2 * sizeof(T);
+  uint32_t w[kW];
+#pragma unroll
+  for (int i = 0; i < kW; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(v[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  if (VEC && sizeof(T) == 4) {  // 32 bytes, a whole sector, at once
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[kW - 4]), "r"(w[kW - 3]), "r"(w[kW - 2]), "r"(w[kW - 1])
+                 : "memory");
+  } else if (VEC) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    T o[8];
+    memcpy(o, w, sizeof(o));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = o[j];
+  }
+}
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kQThreads) mx4_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                    const uint8_t* __restrict__ scales,
                                                                    long long units, uint32_t upr, uint32_t magic,
                                                                    int pitch, T* __restrict__ out, long long ld) {
-  const long long u0 = static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits);
-  const RowOf rows(u0, upr, magic);
-  grid_dep_launch();  // a product that follows sets up meanwhile; it waits for this grid's end
+  const RowOf rows(units, upr, magic);
+  out += rows.row0 * ld;
+  scales += rows.row0 * pitch;
+  const uint32_t* in = reinterpret_cast<const uint32_t*>(codes) + static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits);
+  grid_dep_launch();
   grid_dep_wait();
   uint32_t c[kQUnits], s[kQUnits];
-  long long row[kQUnits];
-  uint32_t unit[kQUnits];
 #pragma unroll
   for (int i = 0; i < kQUnits; ++i) {
     const uint32_t local = i * kQThreads + threadIdx.x;
-    rows.at(local, row[i], unit[i]);
-    if (u0 + local < units) {
-      c[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + (u0 + local) * 4));
-      s[i] = __ldg(scales + row[i] * pitch + (unit[i] >> 2));
+    uint32_t row, unit;
+    rows.at(local, row, unit);
+    if (local < rows.count) {
+      c[i] = __ldg(in + local);
+      s[i] = __ldg(scales + row * pitch + (unit >> 2));
     }
   }
 #pragma unroll
   for (int i = 0; i < kQUnits; ++i) {
-    if (u0 + i * kQThreads + threadIdx.x >= units) continue;
+    const uint32_t local = i * kQThreads + threadIdx.x;
+    if (local >= rows.count) continue;
+    uint32_t row, unit;
+    rows.at(local, row, unit);
     // 2^(s - 127): s = 0 is the subnormal 2^-127, s = 255 is NaN
     const float f = __uint_as_float(s[i] == 0 ? 0x00400000u : s[i] == 255 ? 0x7fffffffu : s[i] << 23);
     float v[8];
     levels8(c[i], v);
-    T o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = from_f32<T>(v[j] * f);
-    T* p = out + row[i] * ld + unit[i] * 8;
-    if (VEC) {
-#pragma unroll
-      for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j)
-        reinterpret_cast<uint4*>(p)[j] = reinterpret_cast<const uint4*>(o)[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = o[j];
+    for (int j = 0; j < 4; ++j) {
+      const float2 q = fmul2(make_float2(v[2 * j], v[2 * j + 1]), make_float2(f, f));
+      v[2 * j] = q.x, v[2 * j + 1] = q.y;
     }
+    store8<T, VEC>(out + row * ld + unit * 8, v);
   }
 }
 
@@ -232,8 +312,9 @@ Units units_of(int rows, int cols) {
   return u;
 }
 
-bool vec_ok(const void* p, size_t ld, size_t size) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * size) % 16 == 0;
+// Whether every row starts on `align` bytes.
+bool vec_ok(const void* p, size_t row_bytes, size_t align) {
+  return reinterpret_cast<uintptr_t>(p) % align == 0 && row_bytes % align == 0;
 }
 
 template <typename T>
@@ -241,11 +322,8 @@ cudaError_t quantize(const void* x, int rows, int cols, size_t ld, uint8_t* code
   const Units u = units_of(rows, cols);
   const T* p = static_cast<const T*>(x);
   const int pitch = mx4_pitch(cols);
-  if (vec_ok(x, ld, sizeof(T)))
-    return launch_dependent(mx4_quantize_kernel<T, true>, u.grid, kQThreads, 0, s, p, ld, u.units, u.upr, u.magic, pitch,
-                            codes, scales);
-  return launch_dependent(mx4_quantize_kernel<T, false>, u.grid, kQThreads, 0, s, p, ld, u.units, u.upr, u.magic, pitch,
-                          codes, scales);
+  return launch_dependent(vec_ok(x, ld * sizeof(T), 16) ? mx4_quantize_kernel<T, true> : mx4_quantize_kernel<T, false>,
+                          u.grid, kQThreads, 0, s, p, ld, u.units, u.upr, u.magic, pitch, codes, scales);
 }
 
 template <typename T>
@@ -254,11 +332,9 @@ cudaError_t dequantize(const uint8_t* codes, const uint8_t* scales, int rows, in
   const Units u = units_of(rows, cols);
   T* p = static_cast<T*>(out);
   const int pitch = mx4_pitch(cols);
-  if (vec_ok(out, ld, sizeof(T)))
-    return launch_dependent(mx4_dequantize_kernel<T, true>, u.grid, kQThreads, 0, s, codes, scales, u.units, u.upr, u.magic, pitch,
-                            p, ld);
-  return launch_dependent(mx4_dequantize_kernel<T, false>, u.grid, kQThreads, 0, s, codes, scales, u.units, u.upr, u.magic, pitch,
-                          p, ld);
+  return launch_dependent(
+      vec_ok(out, ld * sizeof(T), 8 * sizeof(T)) ? mx4_dequantize_kernel<T, true> : mx4_dequantize_kernel<T, false>, u.grid,
+      kQThreads, 0, s, codes, scales, u.units, u.upr, u.magic, pitch, p, ld);
 }
 
 }  // namespace
