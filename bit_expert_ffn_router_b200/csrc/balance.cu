@@ -56,19 +56,27 @@ struct BalanceOut {
   float* prob;      // [E]
 };
 
+__device__ __forceinline__ float ex2(float x) {  // 2^x within 2 steps; 0 below the normal range
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
 // A token's row in a lane group: slot (i, c) of lane s holds expert
 // (i * LANES + s) * 4 + c; slots past E hold -infinity.
-template <int LANES, int SLOTS>
+template <int LANES, int SLOTS, bool VEC>
 struct Row {
   float v[SLOTS * 4];
 
   __device__ __forceinline__ static int expert(int i, int sub) { return (i * LANES + sub) * 4; }
 
-  __device__ __forceinline__ void load(const float* __restrict__ p, int E, int sub, bool vec) {
+  __device__ __forceinline__ void load(const float* __restrict__ p, int E, int sub) {
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       const int e = expert(i, sub);
-      if (vec) {
+      if (VEC) {
         float4 a = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         if (e < E) a = __ldg(reinterpret_cast<const float4*>(p + e));
         v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
@@ -79,21 +87,37 @@ struct Row {
     }
   }
 
+  // exp(x - m) as 2^(x log2(e) - m log2(e)), one multiply-add: what the second
+  // product is rounded by is the same for the whole row and leaves p alone.
+  // Past fp32's range of that product the difference is taken first.
+  struct Exp {
+    float m, off;
+    bool far;
+    __device__ __forceinline__ explicit Exp(float m_) : m(m_ == -INFINITY ? 0.f : m_), off(-m * kLog2e), far(!(fabsf(off) < 1e38f)) {}
+    __device__ __forceinline__ float operator()(float x) const {
+      return far ? ex2((x - m) * kLog2e) : ex2(fmaf(x, kLog2e, off));
+    }
+  };
+
   // v <- exp(v - max); returns the sum (0: nothing above -infinity; NaN if
   // the row holds one) and the maximum.
   __device__ __forceinline__ float exp_sum(float& m) {
-    m = -INFINITY;
+    m = v[0];
 #pragma unroll
-    for (int i = 0; i < SLOTS * 4; ++i) m = fmaxf(m, v[i]);
+    for (int i = 1; i < SLOTS * 4; ++i) m = fmaxf(m, v[i]);
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
+    const Exp e(m);
     float s = 0.f;
+    if (!e.far) {
 #pragma unroll
-    for (int i = 0; i < SLOTS * 4; ++i) {
-      v[i] = __expf(v[i] - base);
-      s += v[i];
+      for (int i = 0; i < SLOTS * 4; ++i) v[i] = ex2(fmaf(v[i], kLog2e, e.off));
+    } else {
+#pragma unroll
+      for (int i = 0; i < SLOTS * 4; ++i) v[i] = e(v[i]);
     }
+#pragma unroll
+    for (int i = 0; i < SLOTS * 4; ++i) s += v[i];
     return group_sum(s, LANES);
   }
 };
@@ -102,8 +126,9 @@ struct Row {
 // [r * per, r * per + per). With one CTA of rows the caller passes its own
 // sums (n_parts = 1) and a grid of one.
 struct Partials {
-  float* sum;    // [n][E]
-  int32_t* cnt;  // [n][E]
+  int pitch;
+  float* sum;    // [n][pitch]: pitch = E rounded up to 4
+  int32_t* cnt;  // [n][pitch]
   double* z;     // [n]
   int32_t* tok;  // [n]
 };
@@ -138,8 +163,9 @@ __device__ __forceinline__ void write_stats(float* stats, double dot, double z, 
   stats[3] = static_cast<float>(static_cast<double>(top) * E / (k * m));
 }
 
-template <int LANES, int SLOTS>
-__global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O, bool vec) {
+template <int LANES, int SLOTS, bool VEC>
+__global__ void __launch_bounds__(kBThreads, SLOTS > 4 ? 1 : 2) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O) {
+  using R_ = Row<LANES, SLOTS, VEC>;
   extern __shared__ float sums[];  // [kBWarps][E]
   __shared__ int hist[kMaxE];
   __shared__ double scratch[kBWarps];
@@ -162,8 +188,8 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
   for (int t0 = (blockIdx.x * kBWarps + warp) * kRows; t0 < R.T; t0 += stride) {
     const int t = t0 + lane / LANES;
     const bool in = t < R.T && (R.mask == nullptr || __ldg(R.mask + t) != 0);
-    Row<LANES, SLOTS> row;
-    row.load(R.logits + static_cast<size_t>(in ? t : 0) * E, E, sub, vec);
+    R_ row;
+    row.load(R.logits + static_cast<size_t>(in ? t : 0) * E, E, sub);
     float m;
     const float s = row.exp_sum(m);
     if (!in || s == 0.f) continue;
@@ -188,7 +214,7 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
   for (int i = 0; i < SLOTS * 4; ++i) {
 #pragma unroll
     for (int o = LANES; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    const int e = Row<LANES, SLOTS>::expert(i / 4, sub) + i % 4;
+    const int e = R_::expert(i / 4, sub) + i % 4;
     if (lane < LANES && e < E) sums[warp * E + e] = acc[i];
   }
   z = block_sum(z, scratch);  // its barriers also publish sums and hist
@@ -197,8 +223,8 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
     for (int e = threadIdx.x; e < E; e += kBThreads) {
       float s = 0.f;
       for (int w = 0; w < kBWarps; ++w) s += sums[w * E + e];
-      P.sum[static_cast<size_t>(blockIdx.x) * E + e] = s;
-      P.cnt[static_cast<size_t>(blockIdx.x) * E + e] = hist[e];
+      P.sum[blockIdx.x * P.pitch + e] = s;
+      P.cnt[blockIdx.x * P.pitch + e] = hist[e];
     }
     if (threadIdx.x == 0) {
       P.z[blockIdx.x] = z;
@@ -223,52 +249,76 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
 }
 
 // The finish over n_parts CTAs' sums: a cluster of kFinCtas CTAs, each over
-// its share of the experts; a warp takes 32 experts of one sixteenth of the
-// parts (coalesced rows), the CTA adds its warps, and CTA 0 adds the CTAs'
-// scalars through distributed shared memory.
+// its share of the experts. A thread adds four experts over every slices-th
+// part with all its loads under way at once, the CTA adds the slices, and CTA 0
+// adds the CTAs' scalars through distributed shared memory. Bound by latency:
+// with one load at a time this kernel took 16 us of a 22 us forward call.
 __global__ void __cluster_dims__(kFinCtas) __launch_bounds__(kBThreads)
     balance_finish_kernel(Partials P, BalanceOut O, int n_parts, int E, int k) {
-  __shared__ double part[kBWarps][32];
-  __shared__ int partc[kBWarps][32];
+  constexpr int kAtOnce = 5;                        // parts of a thread and round
+  __shared__ double part[kBThreads * 4];
+  __shared__ int partc[kBThreads * 4];
   __shared__ double scratch[kBWarps];
   __shared__ int iscratch[kBWarps];
   __shared__ double share_dot;
   __shared__ int share_top;
   cg::cluster_group cluster = cg::this_cluster();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   double z = 0, tok = 0;
   for (int i = threadIdx.x; i < n_parts; i += kBThreads) {
     z += P.z[i];
     tok += P.tok[i];
   }
-  z = block_sum(z, scratch);
+  // `across` threads cover the CTA's experts, four each
+  const int per = (P.pitch / 4 + kFinCtas - 1) / kFinCtas * 4, e0 = blockIdx.x * per;
+  const int across = per / 4, slices = kBThreads / across;
+  const int slice = threadIdx.x / across, c = threadIdx.x - slice * across;
+  const int e = e0 + 4 * c;
+  double s[4] = {0, 0, 0, 0};
+  int n4[4] = {0, 0, 0, 0};
+  if (slice < slices && e < P.pitch) {
+    for (int i0 = slice; i0 < n_parts; i0 += slices * kAtOnce) {
+      float4 a[kAtOnce];
+      int4 b[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        b[j] = make_int4(0, 0, 0, 0);
+        const int i = i0 + j * slices;
+        if (i < n_parts) {
+          a[j] = *reinterpret_cast<const float4*>(P.sum + i * P.pitch + e);
+          b[j] = *reinterpret_cast<const int4*>(P.cnt + i * P.pitch + e);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        s[0] += a[j].x, s[1] += a[j].y, s[2] += a[j].z, s[3] += a[j].w;
+        n4[0] += b[j].x, n4[1] += b[j].y, n4[2] += b[j].z, n4[3] += b[j].w;
+      }
+    }
+  }
+  if (slice < slices) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      part[slice * per + 4 * c + q] = s[q];
+      partc[slice * per + 4 * c + q] = n4[q];
+    }
+  }
+  z = block_sum(z, scratch);  // its barriers also publish the parts
   const int n = static_cast<int>(block_sum(tok, scratch));
   double dot = 0;
   int top = 0;
-  for (int e0 = blockIdx.x * 32; e0 < E; e0 += kFinCtas * 32) {
-    const int e = e0 + lane;
-    double s = 0;
-    int c = 0;
-    if (e < E)
-      for (int i = warp; i < n_parts; i += kBWarps) {
-        s += P.sum[static_cast<size_t>(i) * E + e];
-        c += P.cnt[static_cast<size_t>(i) * E + e];
-      }
-    part[warp][lane] = s;
-    partc[warp][lane] = c;
-    __syncthreads();
-    if (warp == 0 && e < E) {
-      for (int w = 1; w < kBWarps; ++w) {
-        s += part[w][lane];
-        c += partc[w][lane];
-      }
-      dot += s * c;
-      top = max(top, c);
-      O.prob[e] = static_cast<float>(s / max(n, 1));
-      O.counts[e] = c;
+  if (threadIdx.x < per && e0 + threadIdx.x < E) {
+    double t = 0;
+    int m = 0;
+    for (int w = 0; w < slices; ++w) {
+      t += part[w * per + threadIdx.x];
+      m += partc[w * per + threadIdx.x];
     }
-    __syncthreads();
+    dot = t * m;
+    top = m;
+    O.prob[e0 + threadIdx.x] = static_cast<float>(t / max(n, 1));
+    O.counts[e0 + threadIdx.x] = m;
   }
   dot = block_sum(dot, scratch);
   top = block_max(top, iscratch);
@@ -287,11 +337,12 @@ __global__ void __cluster_dims__(kFinCtas) __launch_bounds__(kBThreads)
   cluster.sync();  // the others' shared memory stays until it has been read
 }
 
-template <int LANES, int SLOTS>
-__global__ void __launch_bounds__(kBThreads)
+template <int LANES, int SLOTS, bool VEC>
+__global__ void __launch_bounds__(kBThreads, SLOTS > 4 ? 1 : 2)
     balance_backward_kernel(BalanceRows R, const float* __restrict__ stats, const int32_t* __restrict__ counts,
-                            const float* __restrict__ d_loss, const float* __restrict__ d_gate, bool renorm, bool vec,
+                            const float* __restrict__ d_loss, const float* __restrict__ d_gate, bool renorm,
                             float* __restrict__ d_logits) {
+  using R_ = Row<LANES, SLOTS, VEC>;
   constexpr int kRows = 32 / LANES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
   const int E = R.E, k = R.k;
@@ -302,7 +353,7 @@ __global__ void __launch_bounds__(kBThreads)
   float c[SLOTS * 4];  // ca * counts of this lane's experts
 #pragma unroll
   for (int i = 0; i < SLOTS * 4; ++i) {
-    const int e = Row<LANES, SLOTS>::expert(i / 4, sub) + i % 4;
+    const int e = R_::expert(i / 4, sub) + i % 4;
     c[i] = e < E ? ca * __ldg(counts + e) : 0.f;
   }
   const int stride = gridDim.x * kBWarps * kRows;
@@ -310,36 +361,48 @@ __global__ void __launch_bounds__(kBThreads)
     const int t = t0 + lane / LANES;
     const bool live = t < R.T;
     const bool in = live && (R.mask == nullptr || __ldg(R.mask + t) != 0);
-    Row<LANES, SLOTS> row;
-    row.load(R.logits + static_cast<size_t>(in ? t : 0) * E, E, sub, vec);
+    const size_t at = live ? t : 0;
+    R_ row;
+    row.load(R.logits + at * E, E, sub);
+    // choice j of the row, held by lane j where a row has the whole warp
+    const int32_t* ti = R.idx + at * k;
+    const float* tg = R.gate + at * k;
+    const float* td = d_gate + at * k;
+    int mine = -1;
+    float g = 0.f, gd = 0.f;
+    if (d_gate != nullptr && sub < k) {
+      mine = __ldg(ti + sub);
+      g = __ldg(tg + sub);
+      gd = g * __ldg(td + sub);
+    }
     float m;
     const float s = row.exp_sum(m);
     const bool keep = in && s != 0.f;
     const float r = 1.f / s;
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < SLOTS * 4; ++i) dot += row.v[i] * c[i];
+    for (int i = 0; i < SLOTS * 4; ++i) dot = fmaf(row.v[i], c[i], dot);
     dot = group_sum(dot, LANES) * r;
     // the gates' weighted sum
-    const int32_t* ti = R.idx + static_cast<size_t>(live ? t : 0) * k;
-    const float* tg = R.gate + static_cast<size_t>(live ? t : 0) * k;
-    const float* td = d_gate + static_cast<size_t>(live ? t : 0) * k;
     float gs = 0.f;
     if (d_gate != nullptr) {
-      for (int j = sub; j < k; j += LANES) gs += __ldg(tg + j) * __ldg(td + j);
+      gs = gd;
+      if (LANES < 32)
+        for (int j = sub + LANES; j < k; j += LANES) gs = fmaf(__ldg(tg + j), __ldg(td + j), gs);
       gs = group_sum(gs, LANES);
     }
     // every expert: p * (c_e + base); a z gradient of 0 leaves an infinite lse out
     const float base = (cz != 0.f ? cz * (m + logf(s)) : 0.f) - dot - (renorm ? 0.f : gs);
+    float* out = d_logits + at * E;
     if (live) {
-      float* out = d_logits + static_cast<size_t>(t) * E;
+      const float rb = base * r;
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i) {
-        const int e = Row<LANES, SLOTS>::expert(i, sub);
+        const int e = R_::expert(i, sub);
         float o[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = keep ? row.v[4 * i + q] * r * (c[4 * i + q] + base) : 0.f;
-        if (vec) {
+        for (int q = 0; q < 4; ++q) o[q] = keep ? row.v[4 * i + q] * fmaf(c[4 * i + q], r, rb) : 0.f;
+        if (VEC) {
           if (e < E) *reinterpret_cast<float4*>(out + e) = make_float4(o[0], o[1], o[2], o[3]);
         } else {
 #pragma unroll
@@ -348,22 +411,29 @@ __global__ void __launch_bounds__(kBThreads)
         }
       }
     }
+    if (d_gate == nullptr) continue;
     __syncwarp();  // the stores above come before the chosen experts' below
-    if (d_gate != nullptr && keep) {
-      float* out = d_logits + static_cast<size_t>(t) * E;
-      const float mm = m;
+    const typename R_::Exp ex(m);
+    const float gr = renorm ? gs : 0.f;
+    // An expert that a row names more than once takes the sum of its parts, in
+    // rank order, from each of the lanes that store it.
+    bool again = LANES < 32;
+    if (LANES == 32) {
+      const unsigned same = __match_any_sync(0xffffffffu, mine >= 0 ? mine : -1 - lane);
+      again = __any_sync(0xffffffffu, (same & (same - 1)) != 0);
+    }
+    if (keep) {
       for (int j = sub; j < k; j += LANES) {
-        const int e = __ldg(ti + j);
+        const int e = j == sub ? mine : __ldg(ti + j);
         if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) continue;
-        // an expert named more than once takes the sum of its parts, in rank
-        // order, from each of the lanes that store it
-        float part = 0.f;
-        for (int i = 0; i < k; ++i) {
-          if (__ldg(ti + i) != e) continue;
-          part += __ldg(tg + i) * (__ldg(td + i) - (renorm ? gs : 0.f));
+        float part = gd - g * gr;
+        if (again) {
+          part = 0.f;
+          for (int i = 0; i < k; ++i)
+            if (__ldg(ti + i) == e) part += __ldg(tg + i) * (__ldg(td + i) - gr);
         }
-        const float p = __expf(__ldg(R.logits + static_cast<size_t>(t) * E + e) - mm) * r;
-        out[e] = p * (ca * __ldg(counts + e) + base) + part;
+        const float p = ex(__ldg(R.logits + at * E + e)) * r;
+        out[e] = fmaf(p, fmaf(ca, static_cast<float>(__ldg(counts + e)), base), part);
       }
     }
     __syncwarp();
@@ -372,17 +442,18 @@ __global__ void __launch_bounds__(kBThreads)
 
 bool rows_vec(const void* p, int E) { return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Lanes of a row and float4 per lane, by E.
+// Lanes of a row and float4 per lane by E, and whether rows are float4s.
 template <typename F>
-cudaError_t by_experts(int E, F f) {
+cudaError_t by_experts(int E, bool vec, F f) {
+  auto with = [&](auto lanes, auto slots) { return vec ? f(lanes, slots, std::true_type()) : f(lanes, slots, std::false_type()); };
   using std::integral_constant;
-  if (E <= 16) return f(integral_constant<int, 4>(), integral_constant<int, 1>());
-  if (E <= 32) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
-  if (E <= 64) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
-  if (E <= 128) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
-  if (E <= 256) return f(integral_constant<int, 32>(), integral_constant<int, 2>());
-  if (E <= 512) return f(integral_constant<int, 32>(), integral_constant<int, 4>());
-  return f(integral_constant<int, 32>(), integral_constant<int, 8>());
+  if (E <= 16) return with(integral_constant<int, 4>(), integral_constant<int, 1>());
+  if (E <= 32) return with(integral_constant<int, 8>(), integral_constant<int, 1>());
+  if (E <= 64) return with(integral_constant<int, 16>(), integral_constant<int, 1>());
+  if (E <= 128) return with(integral_constant<int, 32>(), integral_constant<int, 1>());
+  if (E <= 256) return with(integral_constant<int, 32>(), integral_constant<int, 2>());
+  if (E <= 512) return with(integral_constant<int, 32>(), integral_constant<int, 4>());
+  return with(integral_constant<int, 32>(), integral_constant<int, 8>());
 }
 
 int rows_per_warp(int E) { return E <= 16 ? 8 : E <= 32 ? 4 : E <= 64 ? 2 : 1; }
@@ -402,12 +473,15 @@ int balance_ctas(const Ctx& ctx, int E, int T) {
 }  // namespace
 
 size_t balance_ws_bytes(int E) {
-  return static_cast<size_t>(kBalanceMaxCtas) * (static_cast<size_t>(E) * 8 + 16) + 1024;
+  return static_cast<size_t>(kBalanceMaxCtas) * (static_cast<size_t>(E + 3) / 4 * 4 * 8 + 16);
 }
 
 cudaError_t balance_init(const Ctx& ctx) {
   (void)ctx;
-  return cudaFuncSetAttribute(balance_rows_kernel<32, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(balance_rows_kernel<32, 8, true>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBWarps * kMaxE * 4);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(balance_rows_kernel<32, 8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kBWarps * kMaxE * 4);
 }
 
@@ -419,14 +493,14 @@ cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* 
   const BalanceOut O{stats, counts, prob};
   char* b = static_cast<char*>(ws);
   Partials P;
+  P.pitch = (E + 3) / 4 * 4;
   P.z = reinterpret_cast<double*>(b);
   P.sum = reinterpret_cast<float*>(P.z + kBalanceMaxCtas);
-  P.cnt = reinterpret_cast<int32_t*>(P.sum + static_cast<size_t>(kBalanceMaxCtas) * E);
-  P.tok = P.cnt + static_cast<size_t>(kBalanceMaxCtas) * E;
-  const bool vec = rows_vec(logits, E);
-  const cudaError_t e = by_experts(E, [&](auto lanes, auto slots) {
-    return launch_dependent(balance_rows_kernel<lanes.value, slots.value>, n, kBThreads,
-                            static_cast<size_t>(kBWarps) * E * 4, s, R, P, O, vec);
+  P.cnt = reinterpret_cast<int32_t*>(P.sum + static_cast<size_t>(kBalanceMaxCtas) * P.pitch);
+  P.tok = P.cnt + static_cast<size_t>(kBalanceMaxCtas) * P.pitch;
+  const cudaError_t e = by_experts(E, rows_vec(logits, E), [&](auto lanes, auto slots, auto vec) {
+    return launch_dependent(balance_rows_kernel<lanes.value, slots.value, vec.value>, n, kBThreads,
+                            static_cast<size_t>(kBWarps) * E * 4, s, R, P, O);
   });
   if (e != cudaSuccess || n == 1) return e;
   return launch_dependent(balance_finish_kernel, kFinCtas, kBThreads, 0, s, P, O, n, E, c.k);
@@ -438,13 +512,12 @@ cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, cons
                                     cudaStream_t s) {
   const int E = c.E;
   const BalanceRows R{logits, idx, gate, mask, T, E, c.k, ctx.d_status};
-  const bool vec = rows_vec(logits, E) && rows_vec(d_logits, E);
   const int per_cta = kBWarps * rows_per_warp(E);
   const int want = (T + per_cta - 1) / per_cta;
   const int n = want < 2 * ctx.num_sms ? want : 2 * ctx.num_sms;
-  return by_experts(E, [&](auto lanes, auto slots) {
-    return launch_dependent(balance_backward_kernel<lanes.value, slots.value>, n, kBThreads, 0, s, R, stats, counts,
-                            d_loss, d_gate, c.renorm != 0, vec, d_logits);
+  return by_experts(E, rows_vec(logits, E) && rows_vec(d_logits, E), [&](auto lanes, auto slots, auto vec) {
+    return launch_dependent(balance_backward_kernel<lanes.value, slots.value, vec.value>, n, kBThreads, 0, s, R, stats,
+                            counts, d_loss, d_gate, c.renorm != 0, d_logits);
   });
 }
 
