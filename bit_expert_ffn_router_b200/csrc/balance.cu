@@ -25,8 +25,6 @@
 // adds its lane groups in a fixed order, and the finish adds the CTAs'
 // partial sums in fp64, in a fixed order too: results do not depend on the
 // timing. The counts are integer atomics in shared memory.
-#include <cooperative_groups.h>
-
 #include <type_traits>
 
 #include "moe_internal.cuh"
@@ -35,11 +33,11 @@
 namespace moe {
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kBThreads = 512;
+constexpr int kBThreads = 768;  // one CTA per SM leaves 80 registers: a row and the next one's loads
 constexpr int kBWarps = kBThreads / 32;
-constexpr int kFinCtas = 8;  // CTAs of the finish: one cluster
+constexpr int kFinExperts = 32;  // experts of a CTA of the finish
+constexpr int kFinThreads = 256;
+static_assert(kMaxE <= 32 * kFinExperts, "a warp adds up the finish's CTAs");
 
 struct BalanceRows {
   const float* logits;
@@ -122,26 +120,29 @@ struct Row {
   }
 };
 
-// Adds up what the CTAs left behind; one cluster, CTA r finishes the experts
-// [r * per, r * per + per). With one CTA of rows the caller passes its own
-// sums (n_parts = 1) and a grid of one.
+// What the CTAs of the rows' kernel leave behind, and the finish's scalars.
 struct Partials {
   int pitch;
   float* sum;    // [n][pitch]: pitch = E rounded up to 4
   int32_t* cnt;  // [n][pitch]
   double* z;     // [n]
   int32_t* tok;  // [n]
+  double* dot;   // [finish CTAs]
+  int32_t* top;
+  int32_t* ticket;
 };
 
+// Sum over the CTA, in every thread.
 __device__ __forceinline__ double block_sum(double v, double* scratch) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
   __syncthreads();
-  double t = 0;
-  for (int i = 0; i < kBWarps; ++i) t += scratch[i];
-  return t;
+  v = (threadIdx.x & 31) < kBWarps ? scratch[threadIdx.x & 31] : 0.0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 __device__ __forceinline__ int block_max(int v, int* scratch) {
@@ -149,10 +150,42 @@ __device__ __forceinline__ int block_max(int v, int* scratch) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
   __syncthreads();
-  int t = 0;
-  for (int i = 0; i < kBWarps; ++i) t = max(t, scratch[i]);
-  return t;
+  return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < kBWarps ? scratch[threadIdx.x & 31] : 0);
 }
+
+// The rows of a lane group, t0 + stride * i: the row at hand, the next one's
+// logits on their way, and the flag (the mask's byte; 0 past the end) of the
+// one after it. A row that does not count is not read: row 0 stands in.
+template <int LANES, int SLOTS, bool VEC>
+struct Walk {
+  const BalanceRows& R;
+  int t, stride, sub;
+  uint32_t in, ahead, later;
+  Row<LANES, SLOTS, VEC> row, next;
+
+  __device__ __forceinline__ uint32_t flag(int at) const {
+    uint32_t f = at < R.T ? 1u : 0u;
+    if (f != 0 && R.mask != nullptr) f = __ldg(R.mask + at);
+    return f;
+  }
+  __device__ __forceinline__ void fetch(int at, uint32_t f) {
+    next.load(R.logits + static_cast<size_t>(f != 0 ? at : 0) * R.E, R.E, sub);
+  }
+  __device__ __forceinline__ Walk(const BalanceRows& rows, int first, int stride_, int sub_)
+      : R(rows), t(first - stride_), stride(stride_), sub(sub_) {
+    ahead = flag(first);
+    later = flag(first + stride);
+    fetch(first, ahead);
+  }
+  __device__ __forceinline__ void step() {
+    t += stride;
+    in = ahead;
+    ahead = later;
+    row = next;
+    fetch(t + stride, ahead);
+    later = flag(t + 2 * stride);
+  }
+};
 
 // stats from the sums over all experts; one thread.
 __device__ __forceinline__ void write_stats(float* stats, double dot, double z, int n, int top, int E, int k) {
@@ -164,7 +197,7 @@ __device__ __forceinline__ void write_stats(float* stats, double dot, double z, 
 }
 
 template <int LANES, int SLOTS, bool VEC>
-__global__ void __launch_bounds__(kBThreads, SLOTS > 4 ? 1 : 2) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O) {
+__global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O) {
   using R_ = Row<LANES, SLOTS, VEC>;
   extern __shared__ float sums[];  // [kBWarps][E]
   __shared__ int hist[kMaxE];
@@ -184,15 +217,15 @@ __global__ void __launch_bounds__(kBThreads, SLOTS > 4 ? 1 : 2) balance_rows_ker
   double z = 0;
   int n = 0;
   const int stride = gridDim.x * kBWarps * kRows;
+  Walk<LANES, SLOTS, VEC> walk(R, (blockIdx.x * kBWarps + warp) * kRows + lane / LANES, stride, sub);
   // every lane of a warp makes the same number of turns: the shuffles are warp-wide
   for (int t0 = (blockIdx.x * kBWarps + warp) * kRows; t0 < R.T; t0 += stride) {
-    const int t = t0 + lane / LANES;
-    const bool in = t < R.T && (R.mask == nullptr || __ldg(R.mask + t) != 0);
-    R_ row;
-    row.load(R.logits + static_cast<size_t>(in ? t : 0) * E, E, sub);
+    walk.step();
+    const int t = walk.t;
+    R_& row = walk.row;
     float m;
     const float s = row.exp_sum(m);
-    if (!in || s == 0.f) continue;
+    if (walk.in == 0 || s == 0.f) continue;
     const float r = 1.f / s;
 #pragma unroll
     for (int i = 0; i < SLOTS * 4; ++i) acc[i] += row.v[i] * r;
@@ -227,6 +260,7 @@ __global__ void __launch_bounds__(kBThreads, SLOTS > 4 ? 1 : 2) balance_rows_ker
       P.cnt[blockIdx.x * P.pitch + e] = hist[e];
     }
     if (threadIdx.x == 0) {
+      if (blockIdx.x == 0) *P.ticket = 0;
       P.z[blockIdx.x] = z;
       P.tok[blockIdx.x] = n;
     }
@@ -248,97 +282,92 @@ __global__ void __launch_bounds__(kBThreads, SLOTS > 4 ? 1 : 2) balance_rows_ker
   if (threadIdx.x == 0) write_stats(O.stats, dot, z, n, top, E, k);
 }
 
-// The finish over n_parts CTAs' sums: a cluster of kFinCtas CTAs, each over
-// its share of the experts. A thread adds four experts over every slices-th
-// part with all its loads under way at once, the CTA adds the slices, and CTA 0
-// adds the CTAs' scalars through distributed shared memory. Bound by latency:
-// with one load at a time this kernel took 16 us of a 22 us forward call.
-__global__ void __cluster_dims__(kFinCtas) __launch_bounds__(kBThreads)
-    balance_finish_kernel(Partials P, BalanceOut O, int n_parts, int E, int k) {
-  constexpr int kAtOnce = 5;                        // parts of a thread and round
-  __shared__ double part[kBThreads * 4];
-  __shared__ int partc[kBThreads * 4];
-  __shared__ double scratch[kBWarps];
-  __shared__ int iscratch[kBWarps];
-  __shared__ double share_dot;
-  __shared__ int share_top;
-  cg::cluster_group cluster = cg::this_cluster();
+// The finish over n_parts CTAs' sums: a CTA takes kFinExperts experts, a thread
+// four of them over every 32nd part with all its loads under way at once. The
+// CTA that comes last (the rows' kernel set the counter to 0) adds the CTAs'
+// scalars, in the CTAs' order whichever it is. Bound by latency, not by its
+// bytes: with one load at a time it took 16 us of a 22 us forward call.
+__global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(Partials P, BalanceOut O, int n_parts, int E, int k) {
+  constexpr int kAcross = kFinExperts / 4, kSlices = kFinThreads / kAcross;
+  constexpr int kEach = (kBalanceMaxCtas + kSlices - 1) / kSlices;
+  __shared__ double part[kSlices][kFinExperts];
+  __shared__ int partc[kSlices][kFinExperts];
+  __shared__ bool last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = tid % kAcross, slice = tid / kAcross, e = blockIdx.x * kFinExperts + 4 * c;
   grid_dep_wait();
-  double z = 0, tok = 0;
-  for (int i = threadIdx.x; i < n_parts; i += kBThreads) {
-    z += P.z[i];
-    tok += P.tok[i];
-  }
-  // `across` threads cover the CTA's experts, four each
-  const int per = (P.pitch / 4 + kFinCtas - 1) / kFinCtas * 4, e0 = blockIdx.x * per;
-  const int across = per / 4, slices = kBThreads / across;
-  const int slice = threadIdx.x / across, c = threadIdx.x - slice * across;
-  const int e = e0 + 4 * c;
   double s[4] = {0, 0, 0, 0};
   int n4[4] = {0, 0, 0, 0};
-  if (slice < slices && e < P.pitch) {
-    for (int i0 = slice; i0 < n_parts; i0 += slices * kAtOnce) {
-      float4 a[kAtOnce];
-      int4 b[kAtOnce];
+  float4 a[kEach];
+  int4 b[kEach];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        b[j] = make_int4(0, 0, 0, 0);
-        const int i = i0 + j * slices;
-        if (i < n_parts) {
-          a[j] = *reinterpret_cast<const float4*>(P.sum + i * P.pitch + e);
-          b[j] = *reinterpret_cast<const int4*>(P.cnt + i * P.pitch + e);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        s[0] += a[j].x, s[1] += a[j].y, s[2] += a[j].z, s[3] += a[j].w;
-        n4[0] += b[j].x, n4[1] += b[j].y, n4[2] += b[j].z, n4[3] += b[j].w;
-      }
+  for (int j = 0; j < kEach; ++j) {
+    a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    b[j] = make_int4(0, 0, 0, 0);
+    const int i = slice + j * kSlices;
+    if (i < n_parts && e < P.pitch) {
+      a[j] = *reinterpret_cast<const float4*>(P.sum + i * P.pitch + e);
+      b[j] = *reinterpret_cast<const int4*>(P.cnt + i * P.pitch + e);
     }
   }
-  if (slice < slices) {
+  int n = 0;  // tokens that count: every warp adds them up for itself
+  for (int i = lane; i < n_parts; i += 32) n += P.tok[i];
+  n = __reduce_add_sync(0xffffffffu, n);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      part[slice * per + 4 * c + q] = s[q];
-      partc[slice * per + 4 * c + q] = n4[q];
-    }
+  for (int j = 0; j < kEach; ++j) {
+    s[0] += a[j].x, s[1] += a[j].y, s[2] += a[j].z, s[3] += a[j].w;
+    n4[0] += b[j].x, n4[1] += b[j].y, n4[2] += b[j].z, n4[3] += b[j].w;
   }
-  z = block_sum(z, scratch);  // its barriers also publish the parts
-  const int n = static_cast<int>(block_sum(tok, scratch));
-  double dot = 0;
-  int top = 0;
-  if (threadIdx.x < per && e0 + threadIdx.x < E) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    part[slice][4 * c + q] = s[q];
+    partc[slice][4 * c + q] = n4[q];
+  }
+  __syncthreads();
+  if (warp == 0) {
     double t = 0;
     int m = 0;
-    for (int w = 0; w < slices; ++w) {
-      t += part[w * per + threadIdx.x];
-      m += partc[w * per + threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < kSlices; ++w) {
+      t += part[w][lane];
+      m += partc[w][lane];
     }
-    dot = t * m;
-    top = m;
-    O.prob[e0 + threadIdx.x] = static_cast<float>(t / max(n, 1));
-    O.counts[e0 + threadIdx.x] = m;
-  }
-  dot = block_sum(dot, scratch);
-  top = block_max(top, iscratch);
-  if (threadIdx.x == 0) {
-    share_dot = dot;
-    share_top = top;
-  }
-  cluster.sync();
-  if (cluster.block_rank() == 0 && threadIdx.x == 0) {
-    for (int r = 1; r < kFinCtas; ++r) {
-      dot += *cluster.map_shared_rank(&share_dot, r);
-      top = max(top, *cluster.map_shared_rank(&share_top, r));
+    const int x = blockIdx.x * kFinExperts + lane;
+    if (x < E) {
+      O.prob[x] = static_cast<float>(t / max(n, 1));
+      O.counts[x] = m;
+    } else {
+      t = 0;
+      m = 0;
     }
-    write_stats(O.stats, dot, z, n, top, E, k);
+    double dot = t * m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) {
+      P.dot[blockIdx.x] = dot;
+      P.top[blockIdx.x] = m;
+      __threadfence();
+      last = atomicAdd(P.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    }
+    __syncwarp();
+    if (!last) return;
+    __threadfence();
+    double d = lane < gridDim.x ? __ldcg(P.dot + lane) : 0.0, z = 0;
+    m = lane < gridDim.x ? __ldcg(P.top + lane) : 0;
+    for (int i = lane; i < n_parts; i += 32) z += P.z[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      d += __shfl_xor_sync(0xffffffffu, d, o);
+      z += __shfl_xor_sync(0xffffffffu, z, o);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) write_stats(O.stats, d, z, n, m, E, k);
   }
-  cluster.sync();  // the others' shared memory stays until it has been read
 }
 
 template <int LANES, int SLOTS, bool VEC>
-__global__ void __launch_bounds__(kBThreads, SLOTS > 4 ? 1 : 2)
+__global__ void __launch_bounds__(kBThreads)
     balance_backward_kernel(BalanceRows R, const float* __restrict__ stats, const int32_t* __restrict__ counts,
                             const float* __restrict__ d_loss, const float* __restrict__ d_gate, bool renorm,
                             float* __restrict__ d_logits) {
@@ -357,13 +386,12 @@ __global__ void __launch_bounds__(kBThreads, SLOTS > 4 ? 1 : 2)
     c[i] = e < E ? ca * __ldg(counts + e) : 0.f;
   }
   const int stride = gridDim.x * kBWarps * kRows;
+  Walk<LANES, SLOTS, VEC> walk(R, (blockIdx.x * kBWarps + warp) * kRows + lane / LANES, stride, sub);
   for (int t0 = (blockIdx.x * kBWarps + warp) * kRows; t0 < R.T; t0 += stride) {
-    const int t = t0 + lane / LANES;
-    const bool live = t < R.T;
-    const bool in = live && (R.mask == nullptr || __ldg(R.mask + t) != 0);
-    const size_t at = live ? t : 0;
-    R_ row;
-    row.load(R.logits + at * E, E, sub);
+    walk.step();
+    const bool live = walk.t < R.T, in = walk.in != 0;
+    const size_t at = live ? walk.t : 0;
+    R_& row = walk.row;
     // choice j of the row, held by lane j where a row has the whole warp
     const int32_t* ti = R.idx + at * k;
     const float* tg = R.gate + at * k;
@@ -459,30 +487,34 @@ cudaError_t by_experts(int E, bool vec, F f) {
 int rows_per_warp(int E) { return E <= 16 ? 8 : E <= 32 ? 4 : E <= 64 ? 2 : 1; }
 
 // One CTA while each of its lane groups has at most kOneCta rows, else up to
-// two CTAs per SM.
+// one per SM.
 constexpr int kOneCta = 4;
 
 int balance_ctas(const Ctx& ctx, int E, int T) {
   const int per_cta = kBWarps * rows_per_warp(E);
   if (T <= per_cta * kOneCta) return 1;
   const int want = (T + per_cta - 1) / per_cta;
-  const int most = 2 * ctx.num_sms < kBalanceMaxCtas ? 2 * ctx.num_sms : kBalanceMaxCtas;
+  const int most = ctx.num_sms < kBalanceMaxCtas ? ctx.num_sms : kBalanceMaxCtas;
   return want < most ? want : most;
 }
 
 }  // namespace
 
 size_t balance_ws_bytes(int E) {
-  return static_cast<size_t>(kBalanceMaxCtas) * (static_cast<size_t>(E + 3) / 4 * 4 * 8 + 16);
+  return static_cast<size_t>(kBalanceMaxCtas) * (static_cast<size_t>(E + 3) / 4 * 4 * 8 + 16) + 1024;
 }
 
 cudaError_t balance_init(const Ctx& ctx) {
   (void)ctx;
-  const cudaError_t e = cudaFuncSetAttribute(balance_rows_kernel<32, 8, true>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBWarps * kMaxE * 4);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(balance_rows_kernel<32, 8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kBWarps * kMaxE * 4);
+  const void* fns[4] = {reinterpret_cast<const void*>(balance_rows_kernel<32, 4, true>),
+                        reinterpret_cast<const void*>(balance_rows_kernel<32, 4, false>),
+                        reinterpret_cast<const void*>(balance_rows_kernel<32, 8, true>),
+                        reinterpret_cast<const void*>(balance_rows_kernel<32, 8, false>)};
+  for (const void* fn : fns) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kBWarps * kMaxE * 4);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
@@ -495,15 +527,18 @@ cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* 
   Partials P;
   P.pitch = (E + 3) / 4 * 4;
   P.z = reinterpret_cast<double*>(b);
-  P.sum = reinterpret_cast<float*>(P.z + kBalanceMaxCtas);
+  P.sum = reinterpret_cast<float*>(P.z + kBalanceMaxCtas + 32);
   P.cnt = reinterpret_cast<int32_t*>(P.sum + static_cast<size_t>(kBalanceMaxCtas) * P.pitch);
+  P.dot = P.z + kBalanceMaxCtas;
   P.tok = P.cnt + static_cast<size_t>(kBalanceMaxCtas) * P.pitch;
+  P.top = P.tok + kBalanceMaxCtas;
+  P.ticket = P.top + 32;
   const cudaError_t e = by_experts(E, rows_vec(logits, E), [&](auto lanes, auto slots, auto vec) {
     return launch_dependent(balance_rows_kernel<lanes.value, slots.value, vec.value>, n, kBThreads,
                             static_cast<size_t>(kBWarps) * E * 4, s, R, P, O);
   });
   if (e != cudaSuccess || n == 1) return e;
-  return launch_dependent(balance_finish_kernel, kFinCtas, kBThreads, 0, s, P, O, n, E, c.k);
+  return launch_dependent(balance_finish_kernel, (E + kFinExperts - 1) / kFinExperts, kFinThreads, 0, s, P, O, n, E, c.k);
 }
 
 cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
@@ -514,7 +549,7 @@ cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, cons
   const BalanceRows R{logits, idx, gate, mask, T, E, c.k, ctx.d_status};
   const int per_cta = kBWarps * rows_per_warp(E);
   const int want = (T + per_cta - 1) / per_cta;
-  const int n = want < 2 * ctx.num_sms ? want : 2 * ctx.num_sms;
+  const int n = want < ctx.num_sms ? want : ctx.num_sms;
   return by_experts(E, rows_vec(logits, E) && rows_vec(d_logits, E), [&](auto lanes, auto slots, auto vec) {
     return launch_dependent(balance_backward_kernel<lanes.value, slots.value, vec.value>, n, kBThreads, 0, s, R, stats,
                             counts, d_loss, d_gate, c.renorm != 0, d_logits);

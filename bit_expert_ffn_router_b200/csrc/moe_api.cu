@@ -655,6 +655,7 @@ moe_status moe_balance_loss(moe_ctx* ctx, const moe_layer_cfg* cfg, const float*
   if (ctx == nullptr) return MOE_EINVAL;
   const moe_status st = check_cfg_unskipped(cfg);
   if (st != MOE_OK) return st;
+  if (T > kBalanceMaxT) return MOE_EUNSUPPORTED;
   if (T < 0 || stats == nullptr || counts == nullptr || prob == nullptr) return MOE_EINVAL;
   if (!aligned(stats, 4) || !aligned(counts, 4) || !aligned(prob, 4)) return MOE_EINVAL;
   if (T > 0 && (logits == nullptr || idx == nullptr || !aligned(logits, 4) || !aligned(idx, 4))) return MOE_EINVAL;
@@ -673,6 +674,7 @@ moe_status moe_balance_loss_backward(moe_ctx* ctx, const moe_layer_cfg* cfg, con
   if (ctx == nullptr) return MOE_EINVAL;
   const moe_status st = check_cfg_unskipped(cfg);
   if (st != MOE_OK) return st;
+  if (T > kBalanceMaxT) return MOE_EUNSUPPORTED;
   if (T < 0) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
   if (logits == nullptr || idx == nullptr || stats == nullptr || counts == nullptr || d_loss == nullptr ||

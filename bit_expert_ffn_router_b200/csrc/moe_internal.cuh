@@ -19,7 +19,8 @@ constexpr int kMaxK = 32;             // experts per token
 constexpr int kSlotAbsent = -1;       // slot-table value of an expert this device does not hold
 constexpr int kGroupChunk = 512;      // pairs per chunk in the multi-CTA grouping
 constexpr int kTileN = 128;           // tokens per tile of the prefill grouped GEMM
-constexpr int kBalanceMaxCtas = 320;  // CTAs whose partial sums the balance loss keeps in its workspace
+constexpr int kBalanceMaxCtas = 160;  // CTAs whose partial sums the balance loss keeps in its workspace
+constexpr int kBalanceMaxT = 1 << 24;  // tokens of a balance loss (their number is exact in fp32)
 constexpr int kMx4MaxCols = 65536;    // values of a row of an MX matrix
 
 // Device status word codes (word 0 holds the first error seen).
