@@ -153,15 +153,24 @@ __device__ __forceinline__ int block_max(int v, int* scratch) {
   return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < kBWarps ? scratch[threadIdx.x & 31] : 0);
 }
 
-// The rows of a lane group, t0 + stride * i: the row at hand, the next one's
-// logits on their way, and the flag (the mask's byte; 0 past the end) of the
-// one after it. A row that does not count is not read: row 0 stands in.
+// One of a row's choices: choice `sub` in lane `sub` of the row's group.
+struct Choice {
+  int e;
+  float gate, d_gate;
+};
+
+// The rows of a lane group, first + stride * i: the row at hand, the next one's
+// logits and choices on their way, and the flag (the mask's byte; 0 past the
+// end) of the one after it. A row that does not count is not read: row 0
+// stands in.
 template <int LANES, int SLOTS, bool VEC>
 struct Walk {
   const BalanceRows& R;
+  const float* d_gate;  // or null: no gates are loaded
   int t, stride, sub;
   uint32_t in, ahead, later;
   Row<LANES, SLOTS, VEC> row, next;
+  Choice choice, next_choice;
 
   __device__ __forceinline__ uint32_t flag(int at) const {
     uint32_t f = at < R.T ? 1u : 0u;
@@ -169,10 +178,19 @@ struct Walk {
     return f;
   }
   __device__ __forceinline__ void fetch(int at, uint32_t f) {
-    next.load(R.logits + static_cast<size_t>(f != 0 ? at : 0) * R.E, R.E, sub);
+    const size_t r = f != 0 ? at : 0;
+    next.load(R.logits + r * R.E, R.E, sub);
+    next_choice = {-1, 0.f, 0.f};
+    if (sub < R.k) {
+      next_choice.e = __ldg(R.idx + r * R.k + sub);
+      if (d_gate != nullptr) {
+        next_choice.gate = __ldg(R.gate + r * R.k + sub);
+        next_choice.d_gate = __ldg(d_gate + r * R.k + sub);
+      }
+    }
   }
-  __device__ __forceinline__ Walk(const BalanceRows& rows, int first, int stride_, int sub_)
-      : R(rows), t(first - stride_), stride(stride_), sub(sub_) {
+  __device__ __forceinline__ Walk(const BalanceRows& rows, const float* d_gate_, int first, int stride_, int sub_)
+      : R(rows), d_gate(d_gate_), t(first - stride_), stride(stride_), sub(sub_) {
     ahead = flag(first);
     later = flag(first + stride);
     fetch(first, ahead);
@@ -182,6 +200,7 @@ struct Walk {
     in = ahead;
     ahead = later;
     row = next;
+    choice = next_choice;
     fetch(t + stride, ahead);
     later = flag(t + 2 * stride);
   }
@@ -197,7 +216,7 @@ __device__ __forceinline__ void write_stats(float* stats, double dot, double z, 
 }
 
 template <int LANES, int SLOTS, bool VEC>
-__global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O) {
+__global__ void __launch_bounds__(kBThreads, 1) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O) {
   using R_ = Row<LANES, SLOTS, VEC>;
   extern __shared__ float sums[];  // [kBWarps][E]
   __shared__ int hist[kMaxE];
@@ -217,7 +236,7 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
   double z = 0;
   int n = 0;
   const int stride = gridDim.x * kBWarps * kRows;
-  Walk<LANES, SLOTS, VEC> walk(R, (blockIdx.x * kBWarps + warp) * kRows + lane / LANES, stride, sub);
+  Walk<LANES, SLOTS, VEC> walk(R, nullptr, (blockIdx.x * kBWarps + warp) * kRows + lane / LANES, stride, sub);
   // every lane of a warp makes the same number of turns: the shuffles are warp-wide
   for (int t0 = (blockIdx.x * kBWarps + warp) * kRows; t0 < R.T; t0 += stride) {
     walk.step();
@@ -235,7 +254,7 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
       ++n;
     }
     for (int j = sub; j < k; j += LANES) {
-      const int e = __ldg(R.idx + static_cast<size_t>(t) * k + j);
+      const int e = j == sub ? walk.choice.e : __ldg(R.idx + static_cast<size_t>(t) * k + j);
       if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
         atomicAdd(&hist[e], 1);
       else
@@ -367,7 +386,7 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(Partials P,
 }
 
 template <int LANES, int SLOTS, bool VEC>
-__global__ void __launch_bounds__(kBThreads)
+__global__ void __launch_bounds__(kBThreads, 1)
     balance_backward_kernel(BalanceRows R, const float* __restrict__ stats, const int32_t* __restrict__ counts,
                             const float* __restrict__ d_loss, const float* __restrict__ d_gate, bool renorm,
                             float* __restrict__ d_logits) {
@@ -386,7 +405,7 @@ __global__ void __launch_bounds__(kBThreads)
     c[i] = e < E ? ca * __ldg(counts + e) : 0.f;
   }
   const int stride = gridDim.x * kBWarps * kRows;
-  Walk<LANES, SLOTS, VEC> walk(R, (blockIdx.x * kBWarps + warp) * kRows + lane / LANES, stride, sub);
+  Walk<LANES, SLOTS, VEC> walk(R, d_gate, (blockIdx.x * kBWarps + warp) * kRows + lane / LANES, stride, sub);
   for (int t0 = (blockIdx.x * kBWarps + warp) * kRows; t0 < R.T; t0 += stride) {
     walk.step();
     const bool live = walk.t < R.T, in = walk.in != 0;
@@ -396,13 +415,8 @@ __global__ void __launch_bounds__(kBThreads)
     const int32_t* ti = R.idx + at * k;
     const float* tg = R.gate + at * k;
     const float* td = d_gate + at * k;
-    int mine = -1;
-    float g = 0.f, gd = 0.f;
-    if (d_gate != nullptr && sub < k) {
-      mine = __ldg(ti + sub);
-      g = __ldg(tg + sub);
-      gd = g * __ldg(td + sub);
-    }
+    const int mine = walk.choice.e;
+    const float g = walk.choice.gate, gd = g * walk.choice.d_gate;
     float m;
     const float s = row.exp_sum(m);
     const bool keep = in && s != 0.f;
