@@ -45,6 +45,7 @@ constexpr int kBK = 256;                      // K values per stage: 128 bytes o
 constexpr int kMaxGroups = kMaxE + 1;
 constexpr int kList = 256;                    // items of a CTA worked out at its start
 constexpr int kGatherThreads = 32 * kGatherWarps;
+constexpr uint32_t kTryNs = 20000;  // sleep of one try of a wait
 constexpr int kBoxA = 64, kBoxB = 16;                    // x rows of the two TMA boxes
 
 constexpr int kMaxStages = 7;
@@ -55,7 +56,7 @@ struct Table {
   uint64_t x_full[kMaxStages]; // gather threads (count 128), waited on by the x rows' scale warp
   uint64_t empty[kMaxStages];  // MMA commit: codes and scales read
   uint64_t d_full[2];          // MMA commit: accumulator complete
-  uint64_t d_empty[2];         // epilogue (count 256)
+  uint64_t d_empty[2];         // epilogue warps
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
@@ -117,23 +118,36 @@ __device__ __forceinline__ bool aborted(const Table* B) {
   return *reinterpret_cast<const volatile int*>(&B->abort_flag) != 0;
 }
 
-// Waits at most the context's limit; on expiry records the place and raises
-// the CTA's abort flag, on which every role leaves its loop.
+// Whether a wait that has failed so often should go on: until the context's
+// limit has passed or another role has given up; then the place is recorded and
+// the CTA's abort flag raised, on which every role leaves its loop.
+struct Patience {
+  uint64_t deadline = 0;
+  int tries = 0;
+  __device__ __forceinline__ bool more(Table* B, const Params& P, int where) {
+    if (++tries < 8) return true;  // each try sleeps on the barrier for a while
+    if (deadline == 0) deadline = global_timer_ns() + P.timeout_ns;
+    if (aborted(B)) return false;
+    if (global_timer_ns() < deadline) return true;
+    report(P.status, kDevTimeout, 200 + where);
+    *reinterpret_cast<volatile int*>(&B->abort_flag) = 1;
+    return false;
+  }
+};
+
 __device__ __forceinline__ bool wait_bar(Table* B, uint64_t* bar, uint32_t parity, const Params& P, int where) {
-  if (mbar_test(bar, parity)) return true;
-  if (aborted(B)) return false;
-  if (mbar_wait(bar, parity, global_timer_ns() + P.timeout_ns)) return true;
-  report(P.status, kDevTimeout, 200 + where);
-  *reinterpret_cast<volatile int*>(&B->abort_flag) = 1;
-  return false;
+  Patience p;
+  while (!mbar_try_wait(bar, parity, kTryNs))
+    if (!p.more(B, P, where)) return false;
+  return true;
 }
 
 // The same for a whole warp, every lane taking the same path afterwards.
 __device__ __forceinline__ bool wait_warp(Table* B, uint64_t* bar, uint32_t parity, const Params& P, int where) {
-  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = wait_bar(B, bar, parity, P, where) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  Patience p;
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity, kTryNs)))
+    if (!__all_sync(0xffffffffu, p.more(B, P, where))) return false;
+  return true;
 }
 
 template <typename S>
@@ -439,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->d_full[i], 1);
-      mbar_init(&B->d_empty[i], 32 * kEpiWarps);
+      mbar_init(&B->d_empty[i], kEpiWarps);
     }
     mbar_init(&B->mma_done, 1);
     B->abort_flag = 0;
@@ -735,7 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
       }
-      mbar_arrive(&B->d_empty[acc]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->d_empty[acc]);
     }
   }
 
