@@ -158,19 +158,33 @@ __device__ __forceinline__ int tiles_of(int rows) {
 template <typename Sh>
 __device__ void build_table(const Params& P, Table& S) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // The groups' entries are loaded before their number is known (the arrays
+  // have max_uniq of them): one round trip to memory instead of two.
+  const int most = P.grouped ? P.max_uniq + 1 : 1;
+  const int per = (most + kThreads - 1) / kThreads;
+  const int i0 = tid * per;
+  constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
+  int from[kPer + 1], slots[kPer];
+#pragma unroll
+  for (int j = 0; j <= kPer; ++j)
+    if (P.grouped && j <= per && i0 + j <= P.max_uniq) {
+      from[j] = __ldg(P.uniq_offset + i0 + j);
+      if (j < kPer && i0 + j < P.max_uniq) slots[j] = __ldg(P.uniq_slot + i0 + j);
+    }
   const int nu = P.grouped ? min(max(__ldg(P.n_uniq), 0), P.max_uniq) : 0;
   const int ng = P.grouped ? nu + (P.shared_slot >= 0 ? 1 : 0) : 1;
-  const int per = (ng + kThreads - 1) / kThreads;
-  const int i0 = min(tid * per, ng), i1 = min(i0 + per, ng);
   int mine = 0;
-  for (int i = i0; i < i1; ++i) {
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = i0 + j;
+    if (j >= per || i >= ng) break;
     int first, n, slot;
     if (!P.grouped) {
       first = 0, n = P.x_rows, slot = 0;
     } else if (i < nu) {  // bounds hold even where the grouping's arrays do not make sense
-      first = min(max(__ldg(P.uniq_offset + i), 0), P.n_pairs);
-      n = max(min(__ldg(P.uniq_offset + i + 1), P.n_pairs) - first, 0);
-      slot = __ldg(P.uniq_slot + i);
+      first = min(max(from[j], 0), P.n_pairs);
+      n = max(min(from[j + 1], P.n_pairs) - first, 0);
+      slot = slots[j];
     } else {
       first = P.n_pairs, n = P.T, slot = P.shared_slot;
     }
@@ -194,7 +208,7 @@ __device__ void build_table(const Params& P, Table& S) {
   __syncthreads();
   int base = incl - mine;
   for (int w = 0; w < warp; ++w) base += S.scan[w];
-  for (int i = i0; i < i1; ++i) S.prefix[i] += base;
+  for (int i = i0; i < min(i0 + per, ng); ++i) S.prefix[i] += base;
   if (tid == kThreads - 1) {
     S.n_groups = ng;
     S.prefix[ng] = base + mine;
@@ -458,6 +472,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&B->mma_done, 1);
     B->abort_flag = 0;
     fence_mbar_init();
+  }
+  if (threadIdx.x == 32 * kWarpEpi) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tW) : "memory");
+    if (!P.gather) asm volatile("prefetch.tensormap [%0];" ::"l"(&tXa) : "memory");
+    if (!P.gather) asm volatile("prefetch.tensormap [%0];" ::"l"(&tXb) : "memory");
   }
   if (warp == 1) tmem_alloc(&B->tmem_base, 512);
   grid_dep_wait();  // codes, scales and grouping come from the kernels before this one

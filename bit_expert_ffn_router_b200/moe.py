@@ -189,6 +189,7 @@ class Context:
         _check(self.lib.moe_ctx_create(device, ctypes.byref(h)), "moe_ctx_create")
         self.h = h
         self.device = device
+        self._current = None  # of a device: its current stream's handle
 
     def close(self):
         if self.h:
@@ -299,8 +300,10 @@ class Context:
         """The stream's handle; None is the current stream of this context's device."""
         if stream is not None:
             return stream.cuda_stream
-        import torch
-        return torch._C._cuda_getCurrentRawStream(self.device)
+        if self._current is None:
+            import torch
+            self._current = torch._C._cuda_getCurrentRawStream
+        return self._current(self.device)
 
     # -- the router's balance loss -------------------------------------------------
     def balance_loss_status(self, cfg, logits, idx, mask, T, stats, counts, prob, ws, stream=None) -> int:
@@ -311,8 +314,9 @@ class Context:
     def balance_loss(self, cfg, logits, idx, mask, T, stats, counts, prob, ws, stream=None) -> None:
         """moe_balance_loss: stats [4] fp32 (balance loss, z loss, tokens that count, largest load), counts [E]
         int32 and prob [E] fp32 from logits [T, E] fp32, idx [T, k] int32 and mask [T] uint8 or None."""
-        _check(self.balance_loss_status(cfg, logits, idx, mask, T, stats, counts, prob, ws, stream),
-               "moe_balance_loss")
+        status = self.balance_loss_status(cfg, logits, idx, mask, T, stats, counts, prob, ws, stream)
+        if status:
+            raise MoeError(status, "moe_balance_loss")
 
     def balance_loss_backward_status(self, cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate, d_logits,
                                      stream=None) -> int:
@@ -324,32 +328,38 @@ class Context:
                               stream=None) -> None:
         """moe_balance_loss_backward: d_logits [T, E] of d_loss[0] * stats[0] + d_loss[1] * stats[1] and, unless
         d_gate is None, of the gates [T, k]."""
-        _check(self.balance_loss_backward_status(cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate,
-                                                 d_logits, stream), "moe_balance_loss_backward")
+        status = self.balance_loss_backward_status(cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate,
+                                                   d_logits, stream)
+        if status:
+            raise MoeError(status, "moe_balance_loss_backward")
 
     # -- 4-bit experts in the MX format ----------------------------------------------
     def mx4_quantize_status(self, x, codes, scales, stream=None) -> int:
         rows, cols, ld = _rows(x)
         if _bad_mx4(codes, scales, rows, cols):
             return EINVAL
-        return self.lib.moe_mx4_quantize(self.h, x.data_ptr(), _type(x), rows, cols, ld, codes.data_ptr(),
-                                         scales.data_ptr(), self._raw_stream(stream))
+        return self.lib.moe_mx4_quantize(self.h, x.data_ptr(), _type_code(x.dtype, -1), rows, cols, ld,
+                                         codes.data_ptr(), scales.data_ptr(), self._raw_stream(stream))
 
     def mx4_quantize(self, x, codes, scales, stream=None) -> None:
         """moe_mx4_quantize: x [rows, cols] (bf16, fp16 or fp32, any row stride) to codes and scales as
         mx4_buffers gives them."""
-        _check(self.mx4_quantize_status(x, codes, scales, stream), "moe_mx4_quantize")
+        status = self.mx4_quantize_status(x, codes, scales, stream)
+        if status:
+            raise MoeError(status, "moe_mx4_quantize")
 
     def mx4_dequantize_status(self, codes, scales, out, stream=None) -> int:
         rows, cols, ld = _rows(out)
         if _bad_mx4(codes, scales, rows, cols):
             return EINVAL
         return self.lib.moe_mx4_dequantize(self.h, codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
-                                           _type(out), ld, self._raw_stream(stream))
+                                           _type_code(out.dtype, -1), ld, self._raw_stream(stream))
 
     def mx4_dequantize(self, codes, scales, out, stream=None) -> None:
         """moe_mx4_dequantize: the values of codes and scales to out [rows, cols] (bf16, fp16 or fp32)."""
-        _check(self.mx4_dequantize_status(codes, scales, out, stream), "moe_mx4_dequantize")
+        status = self.mx4_dequantize_status(codes, scales, out, stream)
+        if status:
+            raise MoeError(status, "moe_mx4_dequantize")
 
     def mx4_product_status(self, codes, scales, w: "Mx4Matrix", out, grouping=None, shared_slot=-1, gather=False,
                            swiglu=False, gate=False, stream=None) -> int:
@@ -364,14 +374,15 @@ class Context:
         if rows < need:
             return EINVAL
         flags = (MX4_GATHER if gather else 0) | (MX4_SWIGLU if swiglu else 0) | (MX4_GATE if gate else 0)
-        return self.lib.moe_mx4_product(self.h, codes.data_ptr(), scales.data_ptr(), x_rows, ctypes.byref(w.c()), g,
-                                        shared_slot, flags, out.data_ptr(), _type(out), ld, self._raw_stream(stream))
+        return self.lib.moe_mx4_product(self.h, codes.data_ptr(), scales.data_ptr(), x_rows, w.ref, g, shared_slot,
+                                        flags, out.data_ptr(), _type_code(out.dtype, -1), ld, self._raw_stream(stream))
 
     def mx4_product(self, codes, scales, w: "Mx4Matrix", out, grouping=None, shared_slot=-1, gather=False,
                     swiglu=False, gate=False, stream=None) -> None:
         """moe_mx4_product: out = x w^T of 4-bit rows (codes, scales) and the matrices w, one matrix or grouped."""
-        _check(self.mx4_product_status(codes, scales, w, out, grouping, shared_slot, gather, swiglu, gate, stream),
-               "moe_mx4_product")
+        status = self.mx4_product_status(codes, scales, w, out, grouping, shared_slot, gather, swiglu, gate, stream)
+        if status:
+            raise MoeError(status, "moe_mx4_product")
 
     def layer_routing(self, cfg, T, ws, stack_layers=None, layer=0) -> dict:
         """The routing a whole-step call with workspace `ws` computed (moe_layer_routing; with
@@ -496,14 +507,12 @@ def _rows(t):
     raise MoeError(EINVAL, f"a 2-D tensor with contiguous rows is needed, got {tuple(shape)}, {stride}")
 
 
-_type_codes = {}
-
-
-def _type(t) -> int:
-    if not _type_codes:
-        import torch
-        _type_codes.update({torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32})
-    return _type_codes.get(t.dtype, -1)
+def _type_code(dtype, default):
+    """The library's number of a torch dtype; filled in, and replaced by the table's own look-up, on first use."""
+    global _type_code
+    import torch
+    _type_code = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}.get
+    return _type_code(dtype, default)
 
 
 def _bad_mx4(codes, scales, rows, cols) -> bool:
@@ -511,7 +520,7 @@ def _bad_mx4(codes, scales, rows, cols) -> bool:
     that no MX row has is left to the library to refuse)."""
     if cols <= 0 or cols % MX4_BLOCK:
         return False
-    return (codes.shape != (rows, cols // 2) or scales.shape != (rows, (cols // MX4_BLOCK + 15) // 16 * 16)
+    return (codes.numel() != rows * cols // 2 or scales.numel() != rows * ((cols // MX4_BLOCK + 15) // 16 * 16)
             or codes.element_size() != 1 or scales.element_size() != 1
             or not codes.is_contiguous() or not scales.is_contiguous())
 
@@ -548,6 +557,7 @@ class Mx4Matrix:
         self.codes, self.scales = codes, scales
         self._c = _Mx4(codes.data_ptr(), scales.data_ptr(), codes.stride(0), scales.stride(0), self.n_slots, self.rows,
                        cols)
+        self.ref = ctypes.byref(self._c)
 
     def c(self) -> _Mx4:
         return self._c
