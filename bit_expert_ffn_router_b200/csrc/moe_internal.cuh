@@ -141,6 +141,15 @@ __device__ __forceinline__ float2 group_sum2(float2 v, int width) {
   return v;
 }
 
+// A plain load. Kernels that may be set up while the one before them still runs
+// (launch_dependent) read its results this way after their
+// griddepcontrol.wait: a non-coherent load is for data that nobody writes
+// during the kernel's whole life.
+template <typename T>
+__device__ __forceinline__ T ld_plain(const T* p) {
+  return *p;
+}
+
 // Loads that bypass L1 (data written by an earlier kernel of the same stream).
 __device__ __forceinline__ int ld_cg(const int* p) { return __ldcg(p); }
 __device__ __forceinline__ float ld_cg(const float* p) { return __ldcg(p); }

@@ -8,24 +8,39 @@
 // unpacked: codes go from global memory to the tensor cores by TMA, and only
 // the scales (one byte in 17) pass through registers.
 //
-// The weight rows are the M side (128 per tile, TMEM lanes), the x rows the N
-// side (16 to kBN per tile, in steps of 16). A group's rows are cut into equal
-// tiles, so a ragged expert wastes at most 15 rows per tile, one decoded token
-// costs N = 16, and an expert of up to kBN rows reads its weights once.
+// The x rows are the M side (a row per tensor-memory lane, so that a thread of
+// the epilogue owns an output row and finds gate and up of a channel in
+// neighbouring columns), the weight rows the N side, 192 per tile. A group's
+// rows are cut into equal tiles of at most 128; where tokens are few, the MMAs'
+// unused rows cost nothing beside the weights' way from memory (64 x 128 tiles
+// with two stages more: 1 token 8.5 against 9.0 us up and 7.8 against 6.8 down,
+// 64 tokens 92.5 against 90.7 and 55.8 against 49.8). With the weight rows on the M side instead, gate and up
+// sit in neighbouring lanes, and the exchange, the selects and the short stores
+// kept the epilogue four times as long (gate/up of 8192 tokens over 512 experts:
+// 374 us at that step, 289 us after it).
 //
-// One persistent CTA per SM, ten warps:
-//   warp 0     codes: a stage's 128 weight rows x 256 K values by one TMA box,
-//              the x rows by gather loads of four rows each (the rows that the
-//              tokens name, or consecutive ones);
-//   warp 1     TMEM allocation; one lane issues the scale copies
-//              (shared -> tensor memory) and the MMAs;
-//   warps 2-5  scales: thread r loads weight row r's and x rows r's and r +
-//              128's scale bytes, 16 K blocks ahead, and stores them in the
-//              order the tensor memory wants: 512-byte pieces of 128 rows x 4
-//              blocks, row r at (r % 32) * 16 + (r / 32) * 4;
-//   warps 6-9  epilogue: accumulators from tensor memory (two buffers, so that
-//              the next item's MMAs overlap), SwiGLU or gate, one rounding,
-//              stores of 64 to 128 consecutive bytes per row and warp.
+// One persistent CTA per SM; a ring of stages of 256 K values:
+//   warp 0       the weight rows' codes, one TMA box per stage, and the x rows'
+//                in boxes of 64 and 16 where they follow each other;
+//   warp 1       allocates the tensor memory; copies a stage's scales there and
+//                issues its four MMAs;
+//   warps 2-7    scales, to shared memory in the order the copies want: pieces
+//                of 128 rows x 4 blocks, row r at (r % 32) * 16 + (r / 32) * 4;
+//   warps 8-15   epilogue: accumulators from tensor memory (two of them, so that
+//                the next item's MMAs overlap), SwiGLU or gate, one rounding;
+//   warps 16-19  the x rows that tokens name, 16 bytes per copy (TMA gather loads
+//                of four rows took 105 cycles each: 858 us in the place of 626).
+//
+// What bounds it. With few rows per expert, the weights: 64 tokens over 512
+// experts read 613 MB in 91 us. Down products are written at the memory's pace (8192 tokens x
+// 10 experts + shared: 1.19 GB in 201 us, 5.9 TB/s). Gate/up of the same tokens
+// takes 229 us for 1.0 GB (155 us): the gathered rows pass through the
+// load-store units, 16 KB a stage and re-read for each of the 8 weight tiles,
+// and take about 900 cycles a stage where the MMAs take 400. Tried and slower:
+// a pair of CTAs on one tile (cta_group::2; half the weight traffic, but every
+// stage waits for both CTAs: 266 us), scale copies in a warp of their own (their
+// completion lands behind the MMAs in the queue: 309 against 248 us), one gather
+// warp per stage (372 us), 128 weight rows per tile with a stage more (277 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -45,16 +60,21 @@ constexpr int kBK = 256;                      // K values per stage: 128 bytes o
 constexpr int kMaxGroups = kMaxE + 1;
 constexpr int kList = 256;                    // items of a CTA worked out at its start
 constexpr int kGatherThreads = 32 * kGatherWarps;
-constexpr uint32_t kTryNs = 20000;  // sleep of one try of a wait
-constexpr int kBoxA = 64, kBoxB = 16;                    // x rows of the two TMA boxes
-
-constexpr int kMaxStages = 7;
+constexpr uint32_t kTryNs = 20000;            // sleep of one try of a wait
+constexpr int kBoxA = 64, kBoxB = 16;         // x rows of the two TMA boxes
+constexpr int kBM = 128, kBN = 192;           // x rows and weight rows per tile, at most
+constexpr int kStages = 4;
+constexpr int kAcc = kBN;                     // TMEM columns of one accumulator
+constexpr int kPieces = (kBN + 127) / 128;    // of 128 weight rows
+constexpr int kSfCols = 8 + 8 * kPieces;      // TMEM columns of a stage's scales
+constexpr int kGatherRows = kBM / (kGatherThreads / 8);  // rows of a stage per gather thread
+static_assert(2 * kAcc + kStages * kSfCols <= 512, "tensor memory budget");
 
 // The groups' row tiles, laid end to end: group i's first is prefix[i].
 struct Table {
-  uint64_t full[kMaxStages];   // TMA (tx), scale warps: a stage is complete
-  uint64_t x_full[kMaxStages]; // gather threads (count 128), waited on by the x rows' scale warp
-  uint64_t empty[kMaxStages];  // MMA commit: codes and scales read
+  uint64_t full[kStages];   // TMA (tx), scale warps: a stage is complete
+  uint64_t x_full[kStages];  // gather threads (count 128), waited on by the x rows' scale warp
+  uint64_t empty[kStages];  // MMA commit: codes and scales read
   uint64_t d_full[2];          // MMA commit: accumulator complete
   uint64_t d_empty[2];         // epilogue warps
   uint64_t mma_done;
@@ -69,34 +89,20 @@ struct Table {
   alignas(16) int4 list[kList];
 };
 
-// Sizes for tiles of at most BM x rows and BN weight rows, in a ring of STAGES
-// stages. The MMA always takes 128 x rows: with BM = 64 the upper half reads
-// what follows in shared memory, and nobody reads its results.
-template <int BM, int BN, int STAGES>
-struct Shape {
-  static constexpr int kBM = BM;
-  static constexpr int kBN = BN;
-  static constexpr int kStages = STAGES;
-  static constexpr int kAcc = BN;                               // TMEM columns of one accumulator
-  static constexpr int kPieces = (BN + 127) / 128;              // of 128 weight rows
-  static constexpr int kSfCols = 8 + 8 * kPieces;               // TMEM columns of a stage's scales
-  static constexpr int kGatherRows = BM / (kGatherThreads / 8); // rows of a stage per gather thread
-  // a stage in shared memory
-  static constexpr int kX = 0;                          // BM rows x 128 bytes, 128B-swizzled
-  static constexpr int kW = BM * 128;                   // BN rows x 128 bytes
-  static constexpr int kSfX = kW + BN * 128;            // 2 pieces of 512 bytes (K 0..127, 128..255)
-  static constexpr int kSfW = kSfX + 1024;              // 2 x kPieces pieces (K half, 128 weight rows)
+// Shared memory: the stages, the epilogue's staging, the table.
+struct Smem {
+  // within a stage
+  static constexpr int kX = 0;                // kBM rows x 128 bytes, 128B-swizzled
+  static constexpr int kW = kBM * 128;        // kBN rows x 128 bytes
+  static constexpr int kSfX = kW + kBN * 128; // 2 pieces of 512 bytes (K 0..127, 128..255)
+  static constexpr int kSfW = kSfX + 1024;    // 2 x kPieces pieces (K half, 128 weight rows)
   static constexpr int kStage = kSfW + 1024 * kPieces;
-  static constexpr int kOut = STAGES * kStage;          // 32 rows x 128 bytes for each epilogue warp
+  static constexpr int kOut = kStages * kStage;  // 32 rows x 128 bytes for each epilogue warp
   static constexpr int kTable = kOut + kEpiWarps * 4096;
-  static constexpr int kSmem = kTable + static_cast<int>(sizeof(Table)) + 1024;
+  static constexpr int kBytes = kTable + static_cast<int>(sizeof(Table)) + 1024;
   static_assert(kStage % 1024 == 0 && kW % 1024 == 0, "swizzle atoms start on 1024 bytes");
-  static_assert(BM == 128 || BM * 128 + BN * 128 >= 128 * 128, "128 x rows lie inside the stage");
-  static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static_assert(STAGES <= kMaxStages && 2 * kAcc + STAGES * kSfCols <= 512, "tensor memory budget");
+  static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
-using Wide = Shape<128, 192, 4>;
-using Narrow = Shape<64, 128, 6>;
 
 struct Params {
   const uint8_t *xc, *xs, *ws;  // x codes; scales
@@ -150,12 +156,8 @@ __device__ __forceinline__ bool wait_warp(Table* B, uint64_t* bar, uint32_t pari
   return true;
 }
 
-template <typename S>
-__device__ __forceinline__ int tiles_of(int rows) {
-  return (rows + S::kBM - 1) / S::kBM;
-}
+__device__ __forceinline__ int tiles_of(int rows) { return (rows + kBM - 1) / kBM; }
 
-template <typename Sh>
 __device__ void build_table(const Params& P, Table& S) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // The groups' entries are loaded before their number is known (the arrays
@@ -168,10 +170,10 @@ __device__ void build_table(const Params& P, Table& S) {
 #pragma unroll
   for (int j = 0; j <= kPer; ++j)
     if (P.grouped && j <= per && i0 + j <= P.max_uniq) {
-      from[j] = __ldg(P.uniq_offset + i0 + j);
-      if (j < kPer && i0 + j < P.max_uniq) slots[j] = __ldg(P.uniq_slot + i0 + j);
+      from[j] = ld_plain(P.uniq_offset + i0 + j);
+      if (j < kPer && i0 + j < P.max_uniq) slots[j] = ld_plain(P.uniq_slot + i0 + j);
     }
-  const int nu = P.grouped ? min(max(__ldg(P.n_uniq), 0), P.max_uniq) : 0;
+  const int nu = P.grouped ? min(max(ld_plain(P.n_uniq), 0), P.max_uniq) : 0;
   const int ng = P.grouped ? nu + (P.shared_slot >= 0 ? 1 : 0) : 1;
   int mine = 0;
 #pragma unroll
@@ -196,7 +198,7 @@ __device__ void build_table(const Params& P, Table& S) {
     S.rows[i] = n;
     S.slot[i] = slot;
     S.prefix[i] = mine;
-    mine += tiles_of<Sh>(n);
+    mine += tiles_of(n);
   }
   int incl = mine;
 #pragma unroll
@@ -223,7 +225,6 @@ struct Item {
 // Item w: row tile w / w_tiles with weight tile w % w_tiles. The group is the
 // last one whose first tile is at most the tile (empty groups share the next
 // one's); its rows are cut into equal tiles of a multiple of 16.
-template <typename Sh>
 __device__ Item work_out(const Params& P, const Table& S, int w) {
   const int tile = w / P.w_tiles;
   int lo = 0, hi = S.n_groups;
@@ -234,10 +235,10 @@ __device__ Item work_out(const Params& P, const Table& S, int w) {
     else
       hi = mid;
   }
-  const int n = S.rows[lo], nt = tiles_of<Sh>(n), j = tile - S.prefix[lo];
+  const int n = S.rows[lo], nt = tiles_of(n), j = tile - S.prefix[lo];
   const int tr = ((n + nt - 1) / nt + 15) & ~15;
   Item it;
-  it.n0 = (w - tile * P.w_tiles) * Sh::kBN;
+  it.n0 = (w - tile * P.w_tiles) * kBN;
   it.row0 = S.first[lo] + j * tr;
   it.rows = min(tr, n - j * tr);
   it.slot = S.slot[lo];
@@ -245,9 +246,8 @@ __device__ Item work_out(const Params& P, const Table& S, int w) {
 }
 
 // This CTA's i-th item, blockIdx.x + i * gridDim.x.
-template <typename Sh>
 __device__ __forceinline__ Item item_at(const Params& P, const Table& S, int i) {
-  if (i >= kList) return work_out<Sh>(P, S, blockIdx.x + i * gridDim.x);
+  if (i >= kList) return work_out(P, S, blockIdx.x + i * gridDim.x);
   const int4 v = S.list[i];
   return {v.x, v.y, v.z, v.w};
 }
@@ -261,7 +261,7 @@ __device__ __forceinline__ int source_row(const Params& P, int p) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %2, 0;\n\t"
-      "@p ld.global.nc.b32 %0, [%1];\n\t}"
+      "@p ld.global.b32 %0, [%1];\n\t}"
       : "+r"(t)
       : "l"(P.pair_token + p), "r"(P.gather && p < P.n_pairs ? 1 : 0));
   return t;
@@ -427,8 +427,8 @@ __device__ __forceinline__ void store_row(T* p, const uint32_t* w, int valid, in
 // 32 rows of `valid` of N words (lane l has row l's, `rows` rows are real) to
 // p, ld elements from row to row, through the warp's shared memory, so that a
 // store covers 64 or 128 bytes of a row by neighbouring lanes (16 bytes each;
-// the units are swizzled against bank conflicts). Stores of a row per lane
-// instead: fp32 rows of a down product 15% slower.
+// the units are swizzled against bank conflicts). With a row per lane instead,
+// the fp32 rows of a down product of 8192 tokens took 305 us, staged 238 us.
 template <typename T, int N>
 __device__ __forceinline__ void store_staged(uint4* stage, const uint32_t* w, T* p, long long ld, int rows, int valid) {
   constexpr int kUnits = N / 4, kRowsAtOnce = 32 / kUnits;
@@ -448,15 +448,13 @@ __device__ __forceinline__ void store_staged(uint4* stage, const uint32_t* w, T*
   }
 }
 
-template <typename Sh, typename T, bool SWIGLU>
+template <typename T, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
     mx4_product_kernel(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tXa,
                        const __grid_constant__ CUtensorMap tXb, const Params P) {
-  constexpr int kStages = Sh::kStages, kAcc = Sh::kAcc, kGatherRows = Sh::kGatherRows,
-                kPieces = Sh::kPieces;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Table* B = reinterpret_cast<Table*>(smem + Sh::kTable);
+  Table* B = reinterpret_cast<Table*>(smem + Smem::kTable);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -480,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc(&B->tmem_base, 512);
   grid_dep_wait();  // codes, scales and grouping come from the kernels before this one
-  build_table<Sh>(P, *B);
+  build_table(P, *B);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -488,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = B->prefix[B->n_groups] * P.w_tiles;
   const int n_items = total > static_cast<int>(blockIdx.x) ? (total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
   for (int i = threadIdx.x; i < min(n_items, kList); i += kThreads) {
-    const Item it = work_out<Sh>(P, *B, blockIdx.x + i * gridDim.x);
+    const Item it = work_out(P, *B, blockIdx.x + i * gridDim.x);
     B->list[i] = make_int4(it.n0, it.row0, it.rows, it.slot);
   }
   __syncthreads();
@@ -500,23 +498,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       for (int i = 0; i < n_items && ok; ++i) {
-        const Item it = item_at<Sh>(P, *B, i);
-        const uint32_t tx = static_cast<uint32_t>(Sh::kBN + (P.gather ? 0 : it.rows16())) * 128u;
+        const Item it = item_at(P, *B, i);
+        const uint32_t tx = static_cast<uint32_t>(kBN + (P.gather ? 0 : it.rows16())) * 128u;
         for (int k = 0; k < n_k; ++k, ++g) {
           const int st = g % kStages;
           if (g >= kStages && !wait_bar(B, &B->empty[st], ((g / kStages) - 1) & 1, P, 1)) {
             ok = false;
             break;
           }
-          uint8_t* stage = smem + st * Sh::kStage;
+          uint8_t* stage = smem + st * Smem::kStage;
           mbar_arrive_expect_tx(&B->full[st], tx);
-          tma_load_3d(stage + Sh::kW, &tW, k * (kBK / 2), it.n0, it.slot, &B->full[st]);
+          tma_load_3d(stage + Smem::kW, &tW, k * (kBK / 2), it.n0, it.slot, &B->full[st]);
           if (P.gather) continue;
           int r = 0;  // boxes of 64 rows, the rest in boxes of 16
           for (; r + kBoxA <= it.rows16(); r += kBoxA)
-            tma_load_2d(stage + Sh::kX + r * 128, &tXa, k * (kBK / 2), it.row0 + r, &B->full[st]);
+            tma_load_2d(stage + Smem::kX + r * 128, &tXa, k * (kBK / 2), it.row0 + r, &B->full[st]);
           for (; r < it.rows16(); r += kBoxB)
-            tma_load_2d(stage + Sh::kX + r * 128, &tXb, k * (kBK / 2), it.row0 + r, &B->full[st]);
+            tma_load_2d(stage + Smem::kX + r * 128, &tXb, k * (kBK / 2), it.row0 + r, &B->full[st]);
         }
       }
     }
@@ -528,18 +526,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issue
     // The whole warp walks the loop and one lane issues: the operands then stay
-    // in uniform registers, and a stage costs the issuer less than its MMAs take.
-    const uint64_t da0 = smem_desc(smem + Sh::kX), db0 = smem_desc(smem + Sh::kW);
+    // in uniform registers. Issued by one lane of a diverged warp, a stage took
+    // 500 ns whatever its N; now about 310 ns, its MMAs alone 210 ns.
+    const uint64_t da0 = smem_desc(smem + Smem::kX), db0 = smem_desc(smem + Smem::kW);
     const uint32_t hi = static_cast<uint32_t>(da0 >> 32);
     const uint32_t a0 = static_cast<uint32_t>(da0), b0 = static_cast<uint32_t>(db0);
-    const uint64_t dsx = scale_desc(smem + Sh::kSfX), dsw = scale_desc(smem + Sh::kSfW);
+    const uint64_t dsx = scale_desc(smem + Smem::kSfX), dsw = scale_desc(smem + Smem::kSfW);
     const uint32_t hs = static_cast<uint32_t>(dsx >> 32);
     const uint32_t sx = static_cast<uint32_t>(dsx), sw = static_cast<uint32_t>(dsw);
     int st = 0;
     uint32_t ph = 0;
     bool ok = true, ready = false;
     for (int i = 0; i < n_items && ok; ++i) {
-      const int n = min(Sh::kBN, P.w_rows - item_at<Sh>(P, *B, i).n0);
+      const int n = min(kBN, P.w_rows - item_at(P, *B, i).n0);
       const uint32_t id0 = instr_desc_mxf4(n, 0), id1 = instr_desc_mxf4(n, 1);
       const int acc = i & 1;
       if (i >= 2 && !wait_warp(B, &B->d_empty[acc], ((i >> 1) - 1) & 1, P, 2)) break;
@@ -552,8 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t off = static_cast<uint32_t>(st * (Sh::kStage >> 4));
-        const uint32_t sf = tmem + static_cast<uint32_t>(2 * kAcc + st * Sh::kSfCols);
+        const uint32_t off = static_cast<uint32_t>(st * (Smem::kStage >> 4));
+        const uint32_t sf = tmem + static_cast<uint32_t>(2 * kAcc + st * kSfCols);
         if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -597,13 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tok[4];  // x rows of the item that comes next
     auto tokens_of = [&](int i) {
       if (part > 0 || i >= n_items) return;
-      const Item it = item_at<Sh>(P, *B, i);
+      const Item it = item_at(P, *B, i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) tok[j] = source_row(P, it.row0 + min(lane + 32 * j, it.rows - 1));
     };
     const uint8_t* rows[4];
     auto rows_of = [&](int i) {
-      const Item it = item_at<Sh>(P, *B, i);
+      const Item it = item_at(P, *B, i);
       if (part == 0) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -623,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load = [&](int pair) {
       if (part > kPieces) return;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) next[j] = __ldg(reinterpret_cast<const uint4*>(rows[j]) + pair);
+      for (int j = 0; j < 4; ++j) next[j] = ld_plain(reinterpret_cast<const uint4*>(rows[j]) + pair);
     };
     // this warp's turns: every second one of the items' n_pairs_k each
     const int stride = n_pairs_k >= 2 ? 1 : 2;  // items from one that it meets to the next
@@ -656,36 +655,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         load(pair2);
         if (i2 != i) tokens_of(i2 + stride);
       }
-      {
-        int g = i * n_k + 2 * pair;
+      int g = i * n_k + 2 * pair;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (2 * pair + s >= n_k) break;
-          const int st = g % kStages;
-          if (g >= kStages && !wait_warp(B, &B->empty[st], ((g / kStages) - 1) & 1, P, 5)) {
-            ok = false;
-            break;
-          }
-          if (part <= kPieces) {
-            uint8_t* stage = smem + st * Sh::kStage;
-            uint4* p0 = reinterpret_cast<uint4*>(stage + (part == 0 ? Sh::kSfX : Sh::kSfW + 512 * (part - 1))) + lane;
-            uint4* p1 = p0 + (part == 0 ? 512 : 512 * kPieces) / 16;
-            if (s == 0) {
-              *p0 = make_uint4(cur[0].x, cur[1].x, cur[2].x, cur[3].x);
-              *p1 = make_uint4(cur[0].y, cur[1].y, cur[2].y, cur[3].y);
-            } else {
-              *p0 = make_uint4(cur[0].z, cur[1].z, cur[2].z, cur[3].z);
-              *p1 = make_uint4(cur[0].w, cur[1].w, cur[2].w, cur[3].w);
-            }
-          }
-          // the gathered rows' writes are announced with this warp's own
-          if (part == 0 && P.gather && !wait_warp(B, &B->x_full[st], (g / kStages) & 1, P, 7)) {
-            ok = false;
-            break;
-          }
-          arrive_warp(&B->full[st]);  // the stores are read by the asynchronous scale copies
-          ++g;
+      for (int s = 0; s < 2; ++s) {
+        if (2 * pair + s >= n_k) break;
+        const int st = g % kStages;
+        if (g >= kStages && !wait_warp(B, &B->empty[st], ((g / kStages) - 1) & 1, P, 5)) {
+          ok = false;
+          break;
         }
+        if (part <= kPieces) {
+          uint8_t* stage = smem + st * Smem::kStage;
+          uint4* p0 = reinterpret_cast<uint4*>(stage + (part == 0 ? Smem::kSfX : Smem::kSfW + 512 * (part - 1))) + lane;
+          uint4* p1 = p0 + (part == 0 ? 512 : 512 * kPieces) / 16;
+          if (s == 0) {
+            *p0 = make_uint4(cur[0].x, cur[1].x, cur[2].x, cur[3].x);
+            *p1 = make_uint4(cur[0].y, cur[1].y, cur[2].y, cur[3].y);
+          } else {
+            *p0 = make_uint4(cur[0].z, cur[1].z, cur[2].z, cur[3].z);
+            *p1 = make_uint4(cur[0].w, cur[1].w, cur[2].w, cur[3].w);
+          }
+        }
+        // the gathered rows' writes are announced with this warp's own
+        if (part == 0 && P.gather && !wait_warp(B, &B->x_full[st], (g / kStages) & 1, P, 7)) {
+          ok = false;
+          break;
+        }
+        arrive_warp(&B->full[st]);  // the stores are read by the asynchronous scale copies
+        ++g;
       }
       i = i2;
       pair = pair2;
@@ -696,20 +693,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // stage to its swizzled place (chunk ^ row % 8).
     if (P.gather) {
       const int c = threadIdx.x & 7, r0 = (threadIdx.x - 32 * kWarpGather) >> 3;
-      const uint32_t dst0 = smem_u32(smem + Sh::kX) + static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
+      const uint32_t dst0 = smem_u32(smem + Smem::kX) + static_cast<uint32_t>(r0 * 128 + ((c ^ (r0 & 7)) << 4));
       const int row_b = P.K / 2;
       int g = 0;
       bool ok = true;
       int src[kGatherRows], ahead[kGatherRows];  // this item's rows, the next one's
       auto rows_of = [&](int i) {
         if (i >= n_items) return;
-        const Item it = item_at<Sh>(P, *B, i);
+        const Item it = item_at(P, *B, i);
 #pragma unroll
         for (int j = 0; j < kGatherRows; ++j) ahead[j] = source_row(P, it.row0 + min(r0 + 16 * j, it.rows - 1));
       };
       rows_of(0);
       for (int i = 0; i < n_items && ok; ++i) {
-        const Item it = item_at<Sh>(P, *B, i);
+        const Item it = item_at(P, *B, i);
 #pragma unroll
         for (int j = 0; j < kGatherRows; ++j) src[j] = clamp_row(P, ahead[j]);
         rows_of(i + 1);
@@ -722,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = k * (kBK / 2) + c * 16;
           const bool live = col < row_b;
           const uint8_t* base = P.xc + (live ? col : 0);
-          const uint32_t dst = dst0 + static_cast<uint32_t>(st * Sh::kStage);
+          const uint32_t dst = dst0 + static_cast<uint32_t>(st * Smem::kStage);
 #pragma unroll
           for (int j = 0; j < kGatherRows; ++j)
             if (r0 + 16 * j < it.rows)
@@ -740,17 +737,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = q * 32 + lane;
     constexpr int kOut = SWIGLU ? 2 : 1;      // weight rows per result
     constexpr int kWords = 32 / kOut * sizeof(T) / 4;  // of a row's 32 columns
-    uint4* stage_out = reinterpret_cast<uint4*>(smem + Sh::kOut) + 256 * (warp - kWarpEpi);
+    uint4* stage_out = reinterpret_cast<uint4*>(smem + Smem::kOut) + 256 * (warp - kWarpEpi);
     for (int i = 0; i < n_items; ++i) {
-      const Item it = item_at<Sh>(P, *B, i);
+      const Item it = item_at(P, *B, i);
       const int acc = i & 1, p = it.row0 + r;
       const bool live = r < it.rows;
-      const float gate = P.gate && live && p < P.n_pairs ? __ldg(P.pair_gate + p) : 1.f;
+      const float gate = P.gate && live && p < P.n_pairs ? ld_plain(P.pair_gate + p) : 1.f;
       if (!wait_warp(B, &B->d_full[acc], (i >> 1) & 1, P, 6)) break;
       if (q * 32 < it.rows) {
         tc_fence_after();
         const uint32_t base = tmem + static_cast<uint32_t>(acc * kAcc) + (static_cast<uint32_t>(q * 32) << 16);
-        const int n = min(Sh::kBN, P.w_rows - it.n0);
+        const int n = min(kBN, P.w_rows - it.n0);
         for (int c0 = 32 * half; c0 < n; c0 += 64) {
           float v[32];
           uint32_t words[kWords];
@@ -807,17 +804,16 @@ bool map_codes(CUtensorMap* m, const uint8_t* base, int row_bytes, int rows, int
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename Sh, typename T>
+template <typename T>
 const void* kernel_of(bool swiglu) {
-  return swiglu ? reinterpret_cast<const void*>(mx4_product_kernel<Sh, T, true>)
-                : reinterpret_cast<const void*>(mx4_product_kernel<Sh, T, false>);
+  return swiglu ? reinterpret_cast<const void*>(mx4_product_kernel<T, true>)
+                : reinterpret_cast<const void*>(mx4_product_kernel<T, false>);
 }
 
-template <typename Sh>
 const void* kernel_of(int type, bool swiglu) {
-  return type == MOE_TYPE_BF16   ? kernel_of<Sh, __nv_bfloat16>(swiglu)
-         : type == MOE_TYPE_FP16 ? kernel_of<Sh, __half>(swiglu)
-                                 : kernel_of<Sh, float>(swiglu);
+  return type == MOE_TYPE_BF16   ? kernel_of<__nv_bfloat16>(swiglu)
+         : type == MOE_TYPE_FP16 ? kernel_of<__half>(swiglu)
+                                 : kernel_of<float>(swiglu);
 }
 
 }  // namespace
@@ -826,11 +822,8 @@ cudaError_t mx4_product_init(const Ctx& ctx) {
   (void)ctx;
   for (int type = MOE_TYPE_BF16; type <= MOE_TYPE_FP32; ++type)
     for (int swiglu = 0; swiglu < 2; ++swiglu) {
-      cudaError_t e = cudaFuncSetAttribute(kernel_of<Wide>(type, swiglu != 0),
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, Wide::kSmem);
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel_of<Narrow>(type, swiglu != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Narrow::kSmem);
+      const cudaError_t e = cudaFuncSetAttribute(kernel_of(type, swiglu != 0),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kBytes);
       if (e != cudaSuccess) return e;
     }
   return cudaSuccess;
@@ -871,19 +864,14 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   P.ld = static_cast<long long>(a.ld);
   P.status = ctx.d_status;
   P.timeout_ns = ctx.timeout_ns;
-  // Groups of at most 64 rows (no group has more rows than there are tokens,
-  // unless a token names an expert twice): small stages, and more of them in
-  // flight.
-  const bool narrow = (a.g != nullptr ? a.g->T : a.x_rows) <= Narrow::kBM;
-  const int bm = narrow ? Narrow::kBM : Wide::kBM, bn = narrow ? Narrow::kBN : Wide::kBN;
-  P.w_tiles = (a.w.rows + bn - 1) / bn;
-  const long long items = (rows / bm + groups) * P.w_tiles;
+  P.w_tiles = (a.w.rows + kBN - 1) / kBN;
+  const long long items = (rows / kBM + groups) * P.w_tiles;
   if (items > 0x7fffffff) return cudaErrorNotSupported;
 
   const int row_b = a.w.cols / 2;
   CUtensorMap tw, txa, txb;
   const size_t stride = a.w.n_slots > 1 ? a.w.code_stride : static_cast<size_t>(a.w.rows) * row_b;
-  if (!map_codes(&tw, a.w.codes, row_b, a.w.rows, a.w.n_slots, stride, 3, bn)) return cudaErrorInvalidValue;
+  if (!map_codes(&tw, a.w.codes, row_b, a.w.rows, a.w.n_slots, stride, 3, kBN)) return cudaErrorInvalidValue;
   if (a.gather)
     txa = txb = tw;  // not used: the x rows are copied one by one
   else if (!map_codes(&txa, a.x_codes, row_b, a.x_rows, 1, 0, 2, kBoxA) ||
@@ -893,7 +881,7 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items < ctx.num_sms ? items : ctx.num_sms));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = narrow ? Narrow::kSmem : Wide::kSmem;
+  cfg.dynamicSmemBytes = Smem::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -901,8 +889,7 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   void* args[] = {&tw, &txa, &txb, &P};
-  return cudaLaunchKernelExC(
-      &cfg, narrow ? kernel_of<Narrow>(a.out_type, a.swiglu) : kernel_of<Wide>(a.out_type, a.swiglu), args);
+  return cudaLaunchKernelExC(&cfg, kernel_of(a.out_type, a.swiglu), args);
 }
 
 }  // namespace moe

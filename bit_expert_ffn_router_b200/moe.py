@@ -384,6 +384,22 @@ class Context:
         if status:
             raise MoeError(status, "moe_mx4_product")
 
+    def expert_ffn_mx4(self, cfg, x, grouping, up: "Mx4Matrix", down: "Mx4Matrix", shared_slot, bufs, z_rows,
+                       stream=None) -> None:
+        """The expert FFN on 4-bit matrices in the place of expert_ffn (any T): x [T, d] quantised, gate and up
+        rows with SwiGLU (up: [slots, 2f, d], row 2c gate and 2c + 1 up of channel c), the hidden rows
+        quantised, down rows (down: [slots, d, f]) times the gates, to z_rows [n_rows, d] fp32 for combine.
+        shared_slot: the pool slot of the shared expert (-1 where cfg.n_shared is 0); bufs: mx4_ffn_buffers."""
+        if (shared_slot >= 0) != bool(cfg.n_shared) or (up.rows, up.cols, down.rows, down.cols) != (
+                2 * cfg.f, cfg.d, cfg.d, cfg.f):
+            raise MoeError(EINVAL, "expert_ffn_mx4")
+        xq, h, hq = bufs
+        self.mx4_quantize(x, *xq, stream=stream)
+        self.mx4_product(*xq, up, h, grouping=grouping, shared_slot=shared_slot, gather=True, swiglu=True,
+                         stream=stream)
+        self.mx4_quantize(h, *hq, stream=stream)
+        self.mx4_product(*hq, down, z_rows, grouping=grouping, shared_slot=shared_slot, gate=True, stream=stream)
+
     def layer_routing(self, cfg, T, ws, stack_layers=None, layer=0) -> dict:
         """The routing a whole-step call with workspace `ws` computed (moe_layer_routing; with
         stack_layers=L, layer `layer` of a moe_stack_forward workspace), as torch views into ws:
@@ -538,6 +554,15 @@ def mx4_buffers(rows: int, cols: int, device="cuda"):
         raise MoeError(EINVAL if rows < 0 or cols <= 0 else EUNSUPPORTED, "moe_mx4_scale_pitch")
     return (torch.empty(rows, cols // 2, dtype=torch.uint8, device=device),
             torch.empty(rows, pitch, dtype=torch.uint8, device=device))
+
+
+def mx4_ffn_buffers(cfg: LayerCfg, T: int, device="cuda"):
+    """The intermediate rows of expert_ffn_mx4 at T tokens: x's codes and scales, the hidden rows in bf16, and
+    their codes and scales."""
+    import torch
+    n = T * cfg.k + (T if cfg.n_shared else 0)
+    return (mx4_buffers(T, cfg.d, device), torch.empty(n, cfg.f, dtype=torch.bfloat16, device=device),
+            mx4_buffers(n, cfg.f, device))
 
 
 class Mx4Matrix:

@@ -446,7 +446,7 @@ MOE_API size_t moe_mx4_scale_pitch(int cols);
  * 127), values over the scale rounded to the nearest level (ties to the code
  * with an even last bit, magnitudes above 6 to 6). A block of zeros gets s = 0;
  * a block that holds a NaN or an infinity gets s = 255 and codes 0. rows = 0 is
- * a no-op. */
+ * a no-op. codes and scales must not overlap x or each other. */
 MOE_API moe_status moe_mx4_quantize(moe_ctx* ctx, const void* x, int x_type, int rows, int cols, size_t ld,
                                     uint8_t* codes, uint8_t* scales, moe_stream stream);
 
@@ -484,8 +484,8 @@ typedef struct {
  * gate/up half of an expert FFN on 4-bit weights, and with _GATE into fp32
  * rows its down half, which moe_combine joins, as moe_expert_ffn_q2 with
  * z_rows does for 2-bit records. A slot >= w->n_slots or a pair_token outside
- * x is reported as MOE_EDEVICE; its rows are not written (a bad token's row
- * counts as zeros). */
+ * x is reported as MOE_EDEVICE: the slot's rows are not written, the token's row
+ * is that of some other token. out must not overlap the inputs. */
 MOE_API moe_status moe_mx4_product(moe_ctx* ctx, const uint8_t* x_codes, const uint8_t* x_scales, int x_rows,
                                    const moe_mx4_matrix* w, const moe_grouping* grouping, int shared_slot, int flags,
                                    void* out, int out_type, size_t ld, moe_stream stream);

@@ -93,7 +93,8 @@ def pitch(cols):
 def mx4_quantize(x):
     """x [rows, cols] (any float type) -> codes [rows, cols/2], scales [rows, pitch] (uint8)."""
     rows, cols = x.shape
-    v = np.asarray(x, dtype=np.float64).reshape(rows, cols // 32, 32)
+    with np.errstate(invalid="ignore"):  # signalling NaN
+        v = np.asarray(x, dtype=np.float64).reshape(rows, cols // 32, 32)
     q = np.zeros(v.shape, dtype=np.uint8)
     sc = np.zeros((rows, pitch(cols)), dtype=np.uint8)
     for r in range(rows):

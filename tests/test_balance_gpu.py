@@ -1,10 +1,14 @@
 """The router's balance loss and its gradient against the fp64 oracle.
 
-Tolerances, with u = 2^-24 (half a step of fp32). The kernels take exponentials
-of differences x = l - max with an error of at most 2 + 1.173 |x| steps, so
-(4 + 2.4 |x|) u relative; the row's sum of E terms adds E u at most, the
-division u. P(x) below is that sum: the relative error of one p. |x| up to 87:
-beyond, exp(x) is below 2^-125 and the absolute floor covers it.
+Tolerances, with u = 2^-24 (half a step of fp32). The kernels take exp(x), x = l
+- max <= 0, as 2^y with y = l log2(e) - max log2(e): the second product's
+rounding is the same for the whole row (it cancels in p and is worth |max| u in
+lse), y rounds by u |y|, which is u |x| of the result, the constant by half
+that, and 2^y by two steps: (4 + 1.5 |x|) u relative. Taken here as (4 + 2.4
+|x|) u, which covers the documented error of the fast exponential too; the row's
+sum of E terms adds E u at most, the division u. P(x) below is that sum: the
+relative error of one p. |x| up to 87: beyond, exp(x) is below 2^-125 and the
+absolute floor covers it.
 * prob: the mean of the p over the tokens; each p is off by P u p, the sum of T
   terms by T u of itself.
 * stats: the balance loss is a weighted mean of prob with exact weights; lse =

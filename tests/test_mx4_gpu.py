@@ -360,6 +360,108 @@ def test_a_slot_past_the_pool_is_reported_and_not_read():
     assert H.ctx().check_device_status() == M.EDEVICE
 
 
+def test_a_token_past_x_is_reported():
+    G = Grouped(12, 6, 2, 6)
+    w, wv = matrix(G.n_slots, 32, 64, 13)
+    codes, scales = quantize(values(12, 64, 14))
+    xv = O.mx4_values(npy(codes), npy(scales))
+    view = H.ctx().layer_routing(G.cfg, G.T, G.ws)["pair_token"]
+    view[3], view[7] = 12, -1
+    out = torch.full((G.rows(), 32), 7.0, device="cuda")
+    H.ctx().mx4_product(codes, scales, w, out, grouping=G.g, shared_slot=G.shared, gather=True)
+    for rows, tokens, slot, _ in G.parts():
+        keep = [i for i, r in enumerate(rows) if r not in (3, 7)]
+        if keep:
+            assert_product(out[[rows[i] for i in keep]], xv[[tokens[i] for i in keep]], wv[slot], HALF[torch.float32])
+    assert H.ctx().check_device_status() == M.EDEVICE
+    assert H.ctx().last_device_error_detail() in (3, 7)
+
+
+def test_an_expert_named_twice_has_more_rows_than_tokens():
+    """40 tokens that name expert 1 three times each: 120 rows of one group."""
+    T = 40
+    cfg = M.LayerCfg(d=256, f=128, E=4, k=3)
+    idx = torch.ones(T, 3, dtype=torch.int32, device="cuda")
+    gate = torch.rand(T, 3, device="cuda")
+    slots = torch.arange(4, dtype=torch.int32, device="cuda")
+    ws = M.workspace(cfg, T)
+    g = H.ctx().group_tokens(cfg, idx, gate, T, slots, 4, ws)
+    w, wv = matrix(4, 48, 96, 3)
+    codes, scales = quantize(values(T, 96, 4))
+    xv = O.mx4_values(npy(codes), npy(scales))
+    out = torch.empty(T * 3, 48, device="cuda")
+    H.ctx().mx4_product(codes, scales, w, out, grouping=g, gather=True, gate=True)
+    tok = npy(H.ctx().layer_routing(cfg, T, ws)["pair_token"])
+    pg = npy(H.ctx().layer_routing(cfg, T, ws)["pair_gate"]).astype(np.float64)
+    assert_product(out, xv[tok], wv[1], HALF[torch.float32], gate=pg)
+
+
+def test_more_items_than_a_block_lists():
+    """1024 groups of one row by 96 weight tiles: about 660 items per SM."""
+    T, k, E, n = 64, 16, 1024, 18416
+    cfg = M.LayerCfg(d=256, f=128, E=E, k=k)
+    idx = torch.arange(T * k, dtype=torch.int32, device="cuda").view(T, k)
+    gate = torch.rand(T, k, device="cuda")
+    slots = torch.randperm(E, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    ws = M.workspace(cfg, T)
+    g = H.ctx().group_tokens(cfg, idx, gate, T, slots, E, ws)
+    codes, scales = quantize(values(T, 32, 5))
+    wc = torch.randint(0, 256, (E, n, 16), dtype=torch.uint8, device="cuda")
+    wsc = torch.randint(118, 125, (E, n, 16), dtype=torch.uint8, device="cuda")
+    out = torch.empty(T * k, n, device="cuda")
+    H.ctx().mx4_product(codes, scales, M.Mx4Matrix(wc, wsc, 32), out, grouping=g, gather=True)
+    xv = O.mx4_values(npy(codes), npy(scales))
+    for e in (0, 1, 511, 700, 1023):
+        s = int(slots[e])
+        assert_product(out[e:e + 1], xv[e // k:e // k + 1], O.mx4_values(npy(wc[s]), npy(wsc[s])), HALF[torch.float32])
+    # every row against its neighbours' arithmetic: the same x row and matrix through the one-matrix call
+    for e in range(0, E, 41):
+        one = torch.empty(1, n, device="cuda")
+        s = int(slots[e])
+        t = e // k
+        H.ctx().mx4_product(codes[t:t + 1], scales[t:t + 1], M.Mx4Matrix(wc[s], wsc[s], 32), one)
+        assert torch.equal(one[0], out[e])
+    assert H.ctx().check_device_status() == M.OK
+
+
+def test_the_longest_rows():
+    w, wv = matrix(1, 16, 65536, 21)
+    codes, scales = quantize(values(2, 65536, 22))
+    out = torch.empty(2, 16, device="cuda")
+    H.ctx().mx4_product(codes, scales, w, out)
+    assert_product(out, O.mx4_values(npy(codes), npy(scales)), wv[0], HALF[torch.float32])
+
+
+def test_two_captured_products_replayed_at_once():
+    runs = []
+    for i in range(2):
+        G = Grouped(90 + 60 * i, 8, 2, 60 + i)
+        w, _ = matrix(G.n_slots, 256, 512, 25 + i)
+        codes, scales = quantize(values(G.T, 512, 26 + i))
+        out = torch.empty(G.rows(), 128, dtype=torch.bfloat16, device="cuda")
+        call = lambda s=None, a=(codes, scales, w, out, G): H.ctx().mx4_product(  # noqa: E731
+            *a[:4], grouping=a[4].g, shared_slot=a[4].shared, gather=True, swiglu=True, stream=s)
+        call()
+        torch.cuda.synchronize()
+        want = out.clone()
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                for _ in range(4):
+                    call(s)
+        runs.append((graph, s, out, want, G))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, s, out, *_ in runs:
+            with torch.cuda.stream(s):
+                out.zero_()
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, out, want, _ in runs:
+        assert torch.equal(out, want)
+
+
 def test_python_refusals():
     G = Grouped(4, 6, 2, 5)
     w, _ = matrix(G.n_slots, 32, 64, 13)
@@ -383,22 +485,30 @@ def test_python_refusals():
         ctx.mx4_quantize(values(64, 64, 1).t(), *M.mx4_buffers(64, 64))
 
 
+def test_ffn_refusals():
+    G = Grouped(4, 6, 2, 5)
+    cfg = G.cfg
+    up, _ = matrix(G.n_slots, 2 * cfg.f, cfg.d, 13)
+    down, _ = matrix(G.n_slots, cfg.d, cfg.f, 13)
+    x, z = values(4, cfg.d, 1, torch.bfloat16), torch.empty(G.rows(), cfg.d, device="cuda")
+    bufs = M.mx4_ffn_buffers(cfg, 4)
+    for a in ((up, down, -1), (down, down, G.shared), (up, up, G.shared)):
+        with pytest.raises(M.MoeError):
+            H.ctx().expert_ffn_mx4(cfg, x, G.g, *a, bufs, z)
+
+
 # ------------------------------------------------------------------ together
 
 def ffn(G, x, up, down, f, d, y, stream=None, bufs=None):
     """A whole expert step on 4-bit weights: quantise, gate/up, quantise, down, join."""
-    c = H.ctx()
+    c, cfg = H.ctx(), G.cfg.replace(d=d, f=f)
     xq, h, hq, z = bufs
-    c.mx4_quantize(x, *xq, stream=stream)
-    c.mx4_product(*xq, up, h, grouping=G.g, shared_slot=G.shared, gather=True, swiglu=True, stream=stream)
-    c.mx4_quantize(h, *hq, stream=stream)
-    c.mx4_product(*hq, down, z, grouping=G.g, shared_slot=G.shared, gate=True, stream=stream)
-    c.combine(G.cfg.replace(d=d, f=f), G.g, z, x, G.T, y, stream=stream)
+    c.expert_ffn_mx4(cfg, x, G.g, up, down, G.shared, (xq, h, hq), z, stream=stream)
+    c.combine(cfg, G.g, z, x, G.T, y, stream=stream)
 
 
 def ffn_buffers(G, f, d):
-    return (M.mx4_buffers(G.T, d), torch.empty(G.rows(), f, dtype=torch.bfloat16, device="cuda"), M.mx4_buffers(G.rows(), f),
-            torch.empty(G.rows(), d, device="cuda"))
+    return (*M.mx4_ffn_buffers(G.cfg.replace(d=d, f=f), G.T), torch.empty(G.rows(), d, device="cuda"))
 
 
 @pytest.mark.parametrize("T", [1, 3, 8, 77, 400])
