@@ -83,19 +83,17 @@ struct Table {
   int n_groups;
   int scan[kThreads / 32];
   int prefix[kMaxGroups + 1];
-  int first[kMaxGroups];
-  int rows[kMaxGroups];
-  int slot[kMaxGroups];
   alignas(16) int4 list[kList];
 };
 
-// Shared memory: the stages, the epilogue's staging, the table.
+// Shared memory: the stages, the epilogue's staging, the table. (A fifth stage
+// in the place of the staging, which gate/up in 16 bits does not need: no faster.)
 struct Smem {
   // within a stage
-  static constexpr int kX = 0;                // kBM rows x 128 bytes, 128B-swizzled
-  static constexpr int kW = kBM * 128;        // kBN rows x 128 bytes
-  static constexpr int kSfX = kW + kBN * 128; // 2 pieces of 512 bytes (K 0..127, 128..255)
-  static constexpr int kSfW = kSfX + 1024;    // 2 x kPieces pieces (K half, 128 weight rows)
+  static constexpr int kX = 0;                 // kBM rows x 128 bytes, 128B-swizzled
+  static constexpr int kW = kBM * 128;         // kBN rows x 128 bytes
+  static constexpr int kSfX = kW + kBN * 128;  // 2 pieces of 512 bytes (K 0..127, 128..255)
+  static constexpr int kSfW = kSfX + 1024;     // 2 x kPieces pieces (K half, 128 weight rows)
   static constexpr int kStage = kSfW + 1024 * kPieces;
   static constexpr int kOut = kStages * kStage;  // 32 rows x 128 bytes for each epilogue warp
   static constexpr int kTable = kOut + kEpiWarps * 4096;
@@ -194,9 +192,6 @@ __device__ void build_table(const Params& P, Table& S) {
       if (blockIdx.x == 0) report(P.status, kDevBadSlot, first);
       n = 0;
     }
-    S.first[i] = first;
-    S.rows[i] = n;
-    S.slot[i] = slot;
     S.prefix[i] = mine;
     mine += tiles_of(n);
   }
@@ -235,13 +230,20 @@ __device__ Item work_out(const Params& P, const Table& S, int w) {
     else
       hi = mid;
   }
-  const int n = S.rows[lo], nt = tiles_of(n), j = tile - S.prefix[lo];
+  int first = 0, n = P.x_rows, slot = 0;
+  if (P.grouped) {
+    const bool shared = P.shared_slot >= 0 && lo == S.n_groups - 1;
+    first = shared ? P.n_pairs : min(max(ld_plain(P.uniq_offset + lo), 0), P.n_pairs);
+    n = shared ? P.T : min(ld_plain(P.uniq_offset + lo + 1), P.n_pairs) - first;
+    slot = shared ? P.shared_slot : ld_plain(P.uniq_slot + lo);
+  }
+  const int nt = tiles_of(n), j = tile - S.prefix[lo];
   const int tr = ((n + nt - 1) / nt + 15) & ~15;
   Item it;
   it.n0 = (w - tile * P.w_tiles) * kBN;
-  it.row0 = S.first[lo] + j * tr;
+  it.row0 = first + j * tr;
   it.rows = min(tr, n - j * tr);
-  it.slot = S.slot[lo];
+  it.slot = slot;
   return it;
 }
 
@@ -476,6 +478,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!P.gather) asm volatile("prefetch.tensormap [%0];" ::"l"(&tXa) : "memory");
     if (!P.gather) asm volatile("prefetch.tensormap [%0];" ::"l"(&tXb) : "memory");
   }
+  // The x rows that no item fills stay zero: the MMAs take 128 rows whatever an
+  // item has, and on zeros they draw less power (8192 tokens, up to 112 rows a
+  // tile, long runs under the power cap: 303 -> 288 us a pass).
+  if (P.gather) {
+    for (int i = threadIdx.x; i < kStages * kBM * 8; i += kThreads)
+      reinterpret_cast<uint4*>(smem + i / (kBM * 8) * Smem::kStage + Smem::kX)[i % (kBM * 8)] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
   if (warp == 1) tmem_alloc(&B->tmem_base, 512);
   grid_dep_wait();  // codes, scales and grouping come from the kernels before this one
   build_table(P, *B);
@@ -536,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sx = static_cast<uint32_t>(dsx), sw = static_cast<uint32_t>(dsw);
     int st = 0;
     uint32_t ph = 0;
-    bool ok = true, ready = false;
+    bool ok = true;
     for (int i = 0; i < n_items && ok; ++i) {
       const int n = min(kBN, P.w_rows - item_at(P, *B, i).n0);
       const uint32_t id0 = instr_desc_mxf4(n, 0), id1 = instr_desc_mxf4(n, 1);
@@ -546,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * kAcc);
       int left = P.K;  // K values
       for (int k = 0; k < n_k; ++k, left -= kBK) {
-        if (!ready && !wait_warp(B, &B->full[st], ph, P, 3)) {
+        if (!wait_warp(B, &B->full[st], ph, P, 3)) {
           ok = false;
           break;
         }
@@ -574,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           st = 0;
           ph ^= 1;
         }
-        ready = __all_sync(0xffffffffu, mbar_test(&B->full[st], ph));  // the next stage's, while these MMAs run
       }
     }
     // everything issued above completes before the tensor memory is freed
