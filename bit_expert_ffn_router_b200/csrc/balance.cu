@@ -76,17 +76,17 @@ struct Row {
 
   __device__ __forceinline__ static int expert(int i, int sub) { return (i * LANES + sub) * 4; }
 
-  __device__ __forceinline__ void load(const float* __restrict__ p, int E, int sub) {
+  __device__ __forceinline__ void load(const float* p, int E, int sub) {
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       const int e = expert(i, sub);
       if (VEC) {
         float4 a = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (e < E) a = __ldg(reinterpret_cast<const float4*>(p + e));
+        if (e < E) a = ld_plain(reinterpret_cast<const float4*>(p + e));
         v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
       } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[4 * i + c] = e + c < E ? __ldg(p + e + c) : -INFINITY;
+        for (int c = 0; c < 4; ++c) v[4 * i + c] = e + c < E ? ld_plain(p + e + c) : -INFINITY;
       }
     }
   }
@@ -180,7 +180,7 @@ struct Walk {
 
   __device__ __forceinline__ uint32_t flag(int at) const {
     uint32_t f = at < R.T ? 1u : 0u;
-    if (f != 0 && R.mask != nullptr) f = __ldg(R.mask + at);
+    if (f != 0 && R.mask != nullptr) f = ld_plain(R.mask + at);
     return f;
   }
   __device__ __forceinline__ void fetch(int at, uint32_t f) {
@@ -188,10 +188,10 @@ struct Walk {
     next.load(R.logits + r * R.E, R.E, sub);
     next_choice = {-1, 0.f, 0.f};
     if (sub < R.k) {
-      next_choice.e = __ldg(R.idx + r * R.k + sub);
+      next_choice.e = ld_plain(R.idx + r * R.k + sub);
       if (d_gate != nullptr) {
-        next_choice.gate = __ldg(R.gate + r * R.k + sub);
-        next_choice.d_gate = __ldg(d_gate + r * R.k + sub);
+        next_choice.gate = ld_plain(R.gate + r * R.k + sub);
+        next_choice.d_gate = ld_plain(d_gate + r * R.k + sub);
       }
     }
   }
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
   const int E = R.E, k = R.k;
   for (int e = threadIdx.x; e < E; e += kBThreads) hist[e] = 0;
   grid_dep_launch();  // the finish sets up meanwhile; it waits for this grid's end
+  grid_dep_wait();
   __syncthreads();
 
   float acc[SLOTS * 4];
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
       ++n;
     }
     for (int j = sub; j < k; j += LANES) {
-      const int e = j == sub ? walk.choice.e : __ldg(R.idx + static_cast<size_t>(t) * k + j);
+      const int e = j == sub ? walk.choice.e : ld_plain(R.idx + static_cast<size_t>(t) * k + j);
       if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
         atomicAdd(&hist[e], 1);
       else
@@ -392,21 +393,22 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(Partials P,
 
 template <int LANES, int SLOTS, bool VEC>
 __global__ void __launch_bounds__(kBThreads)
-    balance_backward_kernel(BalanceRows R, const float* __restrict__ stats, const int32_t* __restrict__ counts,
-                            const float* __restrict__ d_loss, const float* __restrict__ d_gate, bool renorm,
+    balance_backward_kernel(BalanceRows R, const float* stats, const int32_t* counts, const float* d_loss,
+                            const float* d_gate, bool renorm,
                             float* __restrict__ d_logits) {
   using R_ = Row<LANES, SLOTS, VEC>;
   constexpr int kRows = 32 / LANES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
   const int E = R.E, k = R.k;
-  const float n = fmaxf(__ldg(stats + 2), 1.f);
-  const float ca = __ldg(d_loss) * (static_cast<float>(E) / k) / n / n;
-  const float cz = __ldg(d_loss + 1) * 2.f / n;
+  grid_dep_wait();
+  const float n = fmaxf(ld_plain(stats + 2), 1.f);
+  const float ca = ld_plain(d_loss) * (static_cast<float>(E) / k) / n / n;
+  const float cz = ld_plain(d_loss + 1) * 2.f / n;
   float c[SLOTS * 4];  // ca * counts of this lane's experts
 #pragma unroll
   for (int i = 0; i < SLOTS * 4; ++i) {
     const int e = R_::expert(i / 4, sub) + i % 4;
-    c[i] = e < E ? ca * __ldg(counts + e) : 0.f;
+    c[i] = e < E ? ca * ld_plain(counts + e) : 0.f;
   }
   const int stride = gridDim.x * kBWarps * kRows;
   Walk<LANES, SLOTS, VEC> walk(R, d_gate, (blockIdx.x * kBWarps + warp) * kRows + lane / LANES, stride, sub);
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kBThreads)
     if (d_gate != nullptr) {
       gs = gd;
       if (LANES < 32)
-        for (int j = sub + LANES; j < k; j += LANES) gs = fmaf(__ldg(tg + j), __ldg(td + j), gs);
+        for (int j = sub + LANES; j < k; j += LANES) gs = fmaf(ld_plain(tg + j), ld_plain(td + j), gs);
       gs = group_sum(gs, LANES);
     }
     // every expert: p * (c_e + base); a z gradient of 0 leaves an infinite lse out
@@ -469,16 +471,16 @@ __global__ void __launch_bounds__(kBThreads)
     }
     if (keep) {
       for (int j = sub; j < k; j += LANES) {
-        const int e = j == sub ? mine : __ldg(ti + j);
+        const int e = j == sub ? mine : ld_plain(ti + j);
         if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) continue;
         float part = gd - g * gr;
         if (again) {
           part = 0.f;
           for (int i = 0; i < k; ++i)
-            if (__ldg(ti + i) == e) part += __ldg(tg + i) * (__ldg(td + i) - gr);
+            if (ld_plain(ti + i) == e) part += ld_plain(tg + i) * (ld_plain(td + i) - gr);
         }
-        const float p = ex(__ldg(R.logits + at * E + e)) * r;
-        out[e] = fmaf(p, fmaf(ca, static_cast<float>(__ldg(counts + e)), base), part);
+        const float p = ex(ld_plain(R.logits + at * E + e)) * r;
+        out[e] = fmaf(p, fmaf(ca, static_cast<float>(ld_plain(counts + e)), base), part);
       }
     }
     __syncwarp();
@@ -551,9 +553,8 @@ cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* 
   P.top = P.tok + kBalanceMaxCtas;
   P.ticket = P.top + 32;
   const cudaError_t e = by_experts(E, rows_vec(logits, E), [&](auto lanes, auto slots, auto vec) {
-    balance_rows_kernel<lanes.value, slots.value, vec.value>
-        <<<n, kBThreads, static_cast<size_t>(kBWarps) * E * 4, s>>>(R, P, O);
-    return cudaGetLastError();
+    return launch_dependent(balance_rows_kernel<lanes.value, slots.value, vec.value>, n, kBThreads,
+                            static_cast<size_t>(kBWarps) * E * 4, s, R, P, O);
   });
   if (e != cudaSuccess || n == 1) return e;
   return launch_dependent(balance_finish_kernel, (E + kFinExperts - 1) / kFinExperts, kFinThreads, 0, s, P, O, n, E, c.k);
@@ -569,9 +570,8 @@ cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, cons
   const int want = (T + per_cta - 1) / per_cta;
   const int n = want < ctx.num_sms ? want : ctx.num_sms;
   return by_experts(E, rows_vec(logits, E) && rows_vec(d_logits, E), [&](auto lanes, auto slots, auto vec) {
-    balance_backward_kernel<lanes.value, slots.value, vec.value>
-        <<<n, kBThreads, 0, s>>>(R, stats, counts, d_loss, d_gate, c.renorm != 0, d_logits);
-    return cudaGetLastError();
+    return launch_dependent(balance_backward_kernel<lanes.value, slots.value, vec.value>, n, kBThreads, 0, s, R, stats,
+                            counts, d_loss, d_gate, c.renorm != 0, d_logits);
   });
 }
 
