@@ -32,15 +32,19 @@
 //                of four rows took 105 cycles each: 858 us in the place of 626).
 //
 // What bounds it. With few rows per expert, the weights: 64 tokens over 512
-// experts read 613 MB in 91 us. Down products are written at the memory's pace (8192 tokens x
-// 10 experts + shared: 1.19 GB in 201 us, 5.9 TB/s). Gate/up of the same tokens
-// takes 229 us for 1.0 GB (155 us): the gathered rows pass through the
-// load-store units, 16 KB a stage and re-read for each of the 8 weight tiles,
-// and take about 900 cycles a stage where the MMAs take 400. Tried and slower:
-// a pair of CTAs on one tile (cta_group::2; half the weight traffic, but every
-// stage waits for both CTAs: 266 us), scale copies in a warp of their own (their
-// completion lands behind the MMAs in the queue: 309 against 248 us), one gather
-// warp per stage (372 us), 128 weight rows per tile with a stage more (277 us).
+// experts read 613 MB in 91 us. Down products are written at the memory's pace
+// (8192 tokens x 10 experts + shared: 1.19 GB in 203 us, 5.9 TB/s). One matrix
+// with many rows: the way from L2 (40 KB a stage in about 400 ns on every SM, 15
+// TB/s; 7696 x 1536 x 8192 in 62 us, 3.1 PFLOP/s). Gate/up of 8192 tokens takes
+// 229 us for 1.0 GB (155 us): the gathered rows pass through the load-store
+// units, 16 KB a stage, again for each of the 8 weight tiles, and land about
+// 1700 cycles after they were asked for, where a stage's MMAs take 400.
+//
+// Tried and no faster for gate/up: a pair of CTAs on one tile (cta_group::2: half
+// the weight traffic, but a stage waits for both, 266 us), scale copies in a
+// warp of their own (their completion lands behind the MMAs in the queue: 309
+// against 248 us), a gather warp per stage (372 us), twice the gather warps, a
+// fifth stage, 128 weight rows per tile with a stage more (277 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -61,6 +65,7 @@ constexpr int kMaxGroups = kMaxE + 1;
 constexpr int kList = 256;                    // items of a CTA worked out at its start
 constexpr int kGatherThreads = 32 * kGatherWarps;
 constexpr uint32_t kTryNs = 20000;            // sleep of one try of a wait
+constexpr unsigned long long kDrainNs = 2000000;  // what copies and MMAs in flight get to end, at least
 constexpr int kBoxA = 64, kBoxB = 16;         // x rows of the two TMA boxes
 constexpr int kBM = 128, kBN = 192;           // x rows and weight rows per tile, at most
 constexpr int kStages = 4;
@@ -530,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every copy this warp issued lands before the CTA may exit (bounded wait)
     if (lane == 0) {
-      const uint64_t drain = global_timer_ns() + P.timeout_ns;
+      const uint64_t drain = global_timer_ns() + max(P.timeout_ns, kDrainNs);
       for (int n = max(0, g - kStages); n < g; ++n) mbar_wait(&B->full[n % kStages], (n / kStages) & 1, drain);
     }
   } else if (warp == 1) {
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // everything issued above completes before the tensor memory is freed
     if (elect_one()) tc_commit(&B->mma_done);
     __syncwarp();
-    if (lane == 0) mbar_wait(&B->mma_done, 0, global_timer_ns() + P.timeout_ns);
+    if (lane == 0) mbar_wait(&B->mma_done, 0, global_timer_ns() + max(P.timeout_ns, kDrainNs));
     __syncwarp();
   } else if (warp < kWarpEpi) {
     // ---------------------------------------------------------- scales
