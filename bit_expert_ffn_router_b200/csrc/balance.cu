@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
   const int E = R.E, k = R.k;
   for (int e = threadIdx.x; e < E; e += kBThreads) hist[e] = 0;
-  grid_dep_launch();  // the finish sets up meanwhile; it waits for this grid's end
   grid_dep_wait();
+  grid_dep_launch();  // the finish sets up meanwhile; it waits for this grid's end
   __syncthreads();
 
   float acc[SLOTS * 4];

@@ -191,8 +191,10 @@ __global__ void __launch_bounds__(kQThreads) mx4_quantize_kernel(const T* x, lon
   x += ROWS == kFlat ? static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits * 8) : rows.row0 * ld;
   scales += rows.row0 * pitch;
   uint32_t* out = reinterpret_cast<uint32_t*>(codes) + static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits);
-  grid_dep_launch();  // a product that follows sets up meanwhile; it waits for this grid's end
   grid_dep_wait();
+  // a product that follows sets up meanwhile and waits for this grid's end; what
+  // came before this grid has ended by now, so nothing of it is overtaken
+  grid_dep_launch();
   Values<T> v[kQUnits];
 #pragma unroll
   for (int i = 0; i < kQUnits; ++i) {
@@ -277,8 +279,7 @@ __global__ void __launch_bounds__(kQThreads) mx4_dequantize_kernel(const uint8_t
   out += rows.row0 * ld;
   scales += rows.row0 * pitch;
   const uint32_t* in = reinterpret_cast<const uint32_t*>(codes) + static_cast<long long>(blockIdx.x) * (kQThreads * kQUnits);
-  grid_dep_launch();
-  grid_dep_wait();
+  grid_dep_wait();  // and no early launch of the next: what is written here may be anything
   uint32_t c[kQUnits], s[kQUnits];
 #pragma unroll
   for (int i = 0; i < kQUnits; ++i) {

@@ -573,7 +573,7 @@ class Mx4Matrix:
         if codes.dim() == 2:
             codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
         pitch = mx4_scale_pitch(cols)
-        if pitch == 0 or codes.dim() != 3 or scales.dim() != 3:
+        if pitch == 0 or codes.dim() != 3 or scales.dim() != 3 or codes.shape[0] == 0:
             raise MoeError(EINVAL, "Mx4Matrix")
         self.n_slots, self.rows, self.cols = codes.shape[0], codes.shape[1], cols
         for t, n in ((codes, cols // 2), (scales, pitch)):
