@@ -36,15 +36,19 @@
 // (8192 tokens x 10 experts + shared: 1.19 GB in 203 us, 5.9 TB/s). One matrix
 // with many rows: the way from L2 (40 KB a stage in about 400 ns on every SM, 15
 // TB/s; 7696 x 1536 x 8192 in 62 us, 3.1 PFLOP/s). Gate/up of 8192 tokens takes
-// 229 us for 1.0 GB (155 us): the gathered rows pass through the load-store
-// units, 16 KB a stage, again for each of the 8 weight tiles, and land about
-// 1700 cycles after they were asked for, where a stage's MMAs take 400.
+// 229 us for 1.0 GB (155 us): of a stage's 530 ns about 35 are the gathered rows
+// (16-byte copies by the load-store units, again for each of the 8 weight tiles),
+// 30 the epilogue, 210 the MMAs, and the rest the way of codes and scales
+// through the ring. Where the rows follow each other, 16 experts' worth takes 82
+// us (3.6 PFLOP/s), gathered 96.
 //
 // Tried and no faster for gate/up: a pair of CTAs on one tile (cta_group::2: half
-// the weight traffic, but a stage waits for both, 266 us), scale copies in a
-// warp of their own (their completion lands behind the MMAs in the queue: 309
-// against 248 us), a gather warp per stage (372 us), twice the gather warps, a
-// fifth stage, 128 weight rows per tile with a stage more (277 us).
+// the weight traffic, but a stage waits for both, 266 us), x rows that stay for
+// all weight tiles of their row tile (three stages of weight rows are left: 238
+// us), scale copies in a warp of their own (their completion lands behind the
+// MMAs in the queue: 309 against 248 us), a gather warp per stage (372 us), twice
+// the gather warps, a fifth stage, 128 weight rows per tile with a stage more (277
+// us), one arrival per warp a stage late (260 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
