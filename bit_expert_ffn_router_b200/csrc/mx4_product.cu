@@ -92,6 +92,9 @@ struct Table {
   int n_groups;
   int scan[kThreads / 32];
   int prefix[kMaxGroups + 1];
+  int first[kMaxGroups];
+  int rows[kMaxGroups];
+  int slot[kMaxGroups];
   alignas(16) int4 list[kList];
 };
 
@@ -201,6 +204,9 @@ __device__ void build_table(const Params& P, Table& S) {
       if (blockIdx.x == 0) report(P.status, kDevBadSlot, first);
       n = 0;
     }
+    S.first[i] = first;
+    S.rows[i] = n;
+    S.slot[i] = slot;
     S.prefix[i] = mine;
     mine += tiles_of(n);
   }
@@ -239,20 +245,13 @@ __device__ Item work_out(const Params& P, const Table& S, int w) {
     else
       hi = mid;
   }
-  int first = 0, n = P.x_rows, slot = 0;
-  if (P.grouped) {
-    const bool shared = P.shared_slot >= 0 && lo == S.n_groups - 1;
-    first = shared ? P.n_pairs : min(max(ld_plain(P.uniq_offset + lo), 0), P.n_pairs);
-    n = shared ? P.T : min(ld_plain(P.uniq_offset + lo + 1), P.n_pairs) - first;
-    slot = shared ? P.shared_slot : ld_plain(P.uniq_slot + lo);
-  }
-  const int nt = tiles_of(n), j = tile - S.prefix[lo];
+  const int n = S.rows[lo], nt = tiles_of(n), j = tile - S.prefix[lo];
   const int tr = ((n + nt - 1) / nt + 15) & ~15;
   Item it;
   it.n0 = (w - tile * P.w_tiles) * kBN;
-  it.row0 = first + j * tr;
+  it.row0 = S.first[lo] + j * tr;
   it.rows = min(tr, n - j * tr);
-  it.slot = slot;
+  it.slot = S.slot[lo];
   return it;
 }
 
