@@ -67,6 +67,7 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x within 2 steps; 0 below 
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFar = 65536.f;  // below it the sum is scaled by 2^(2^-9) at most
 
 // A token's row in a lane group: slot (i, c) of lane s holds expert
 // (i * LANES + s) * 4 + c; slots past E hold -infinity.
@@ -92,12 +93,14 @@ struct Row {
   }
 
   // exp(x - m) as 2^(x log2(e) - m log2(e)), one multiply-add: what the second
-  // product is rounded by is the same for the whole row and leaves p alone.
-  // Past fp32's range of that product the difference is taken first.
+  // product is rounded by is the same for the whole row and leaves p alone. It
+  // does scale the row's sum by 2^r, |r| <= 2^-25 |m log2(e)|, so rows that lie
+  // far out take the difference first: past 1e10 the sum would leave fp32's
+  // range, and a row would count as empty.
   struct Exp {
     float m, off;
     bool far;
-    __device__ __forceinline__ explicit Exp(float m_) : m(m_ == -INFINITY ? 0.f : m_), off(-m * kLog2e), far(!(fabsf(off) < 1e38f)) {}
+    __device__ __forceinline__ explicit Exp(float m_) : m(m_ == -INFINITY ? 0.f : m_), off(-m * kLog2e), far(!(fabsf(off) < kFar)) {}
     __device__ __forceinline__ float operator()(float x) const {
       return far ? ex2((x - m) * kLog2e) : ex2(fmaf(x, kLog2e, off));
     }

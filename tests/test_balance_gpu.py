@@ -166,6 +166,30 @@ def test_masks_of_the_lowest_value_and_wide_logits():
     assert np.isinf(stats[1]) and np.isfinite(stats[0]) and np.isfinite(d).all()
 
 
+@pytest.mark.parametrize("T,E,k", [(40, 16, 2), (900, 16, 2), (64, 61, 3), (300, 256, 4), (900, 512, 10), (50, 1024, 32)])
+@pytest.mark.parametrize("renorm", [True, False], ids=["renorm", "full"])
+def test_rows_far_from_zero(T, E, k, renorm):
+    """A row's maximum times log2(e) has a rounding that leaves fp32's exponents from about 1e10 on; the sums must
+    not depend on it. Whole rows at such values (a mask added to every logit), and single logits far above the rest."""
+    c = make(T, E, k, seed=12, renorm=renorm)
+    l = c["l"]
+    for i, far in enumerate((3e4, -7e4, 2e6, 1e10, -1e10, 2e10, 4e12, -1e18)):
+        l[i] += np.float32(far)
+    l[8, 3], l[9, 5], l[10, 1], l[11, 2] = 1e9, 2e10, 1e15, 7e17
+    l[12, :5], l[12, 5:] = 1e12, -1e12
+    check(c, Run(c)().out())
+    # the z loss of these is past fp32; everything else is not
+    l[13], l[14], l[15, 1] = -1e30, 1e30, 1e30
+    l[16, :5], l[16, 5:] = 3e38, -3e38
+    l[17, :] = np.finfo(np.float32).max
+    c["d_loss"][1] = 0
+    stats, counts, prob, d = Run(c)().out()
+    assert np.isinf(stats[1])
+    stats = stats.astype(np.float64)
+    stats[1] = O.balance(l, c["idx"], c["mask"])[0][1]
+    check(c, (stats, counts, prob, d))
+
+
 def test_nan_logits_show():
     c = make(30, 16, 2, seed=10)
     c["l"][4, 3] = np.nan
