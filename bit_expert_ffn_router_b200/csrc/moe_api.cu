@@ -747,7 +747,9 @@ moe_status moe_mx4_product(moe_ctx* ctx, const uint8_t* x_codes, const uint8_t* 
     if (shared_slot != -1 || (flags & (MOE_MX4_GATHER | MOE_MX4_GATE)) != 0) return MOE_EINVAL;
   } else {
     const moe_grouping& g = *grouping;
-    if (g.T < 0 || g.k <= 0 || g.k > kMaxK || g.E <= 0 || g.E > kMaxE || g.n_pairs != g.T * g.k) return MOE_EINVAL;
+    if (g.T < 0 || g.k <= 0 || g.k > kMaxK || g.E <= 0 || g.E > kMaxE ||
+        g.n_pairs != static_cast<long long>(g.T) * g.k)
+      return MOE_EINVAL;
     if (shared_slot < -1 || shared_slot >= w->n_slots) return MOE_EINVAL;
     out_rows = static_cast<long long>(g.n_pairs) + (shared_slot >= 0 ? g.T : 0);
     if ((flags & MOE_MX4_GATHER) != 0 ? x_rows != g.T : x_rows < out_rows) return MOE_EINVAL;
@@ -755,6 +757,7 @@ moe_status moe_mx4_product(moe_ctx* ctx, const uint8_t* x_codes, const uint8_t* 
                     g.pair_token == nullptr || g.pair_gate == nullptr))
       return MOE_EINVAL;
   }
+  if (out_rows > 1 << 30) return MOE_EUNSUPPORTED;  // row numbers, sums of two among them, are ints
   if (out_rows == 0) return MOE_OK;
   if (x_codes == nullptr || x_scales == nullptr || !aligned(x_codes, 16) || !aligned(x_scales, 16)) return MOE_EINVAL;
   const size_t out_cols = static_cast<size_t>((flags & MOE_MX4_SWIGLU) != 0 ? w->rows / 2 : w->rows);

@@ -480,7 +480,7 @@ typedef struct {
  *     output row's own number (x_rows >= the output rows). Rows of pairs that
  *     the grouping left out (MOE_SLOT_ABSENT) are left as they were.
  * out: [.., w->rows], or w->rows / 2 columns with MOE_MX4_SWIGLU; ld elements
- * from row to row; aligned to its element. With _GATHER | _SWIGLU this is the
+ * from row to row; aligned to its element; at most 2^30 rows. With _GATHER | _SWIGLU this is the
  * gate/up half of an expert FFN on 4-bit weights, and with _GATE into fp32
  * rows its down half, which moe_combine joins, as moe_expert_ffn_q2 with
  * z_rows does for 2-bit records. A slot >= w->n_slots or a pair_token outside

@@ -158,6 +158,15 @@ def test_grouped_product_refusals():
     assert _product(g=_grouping(T=0), x_rows=0) == M.OK
 
 
+def test_grouped_product_sizes_past_32_bits():
+    # T * k that wraps around to n_pairs; output rows that no int numbers
+    t = (1 << 28) + 1
+    assert _product(g=_grouping(T=t, k=16, n_pairs=16, n_rows=16 + t), x_rows=t, flags=M.MX4_GATHER) == M.EINVAL
+    t = 1 << 30
+    assert _product(g=_grouping(T=t, k=1), x_rows=t, shared=3, flags=M.MX4_GATHER) == M.EUNSUPPORTED
+    assert _product(x_rows=t + 1) == M.EUNSUPPORTED
+
+
 def test_matrix_and_buffer_checks():
     import torch
     with pytest.raises(M.MoeError):
