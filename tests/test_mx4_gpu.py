@@ -576,3 +576,40 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for *_, y, want, s in runs:
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,absent,n_shared", [(5, (0, 3, 5), 1), (90, (0, 3, 5), 1), (7, (), 0), (300, (1,), 0),
+                                               (4, tuple(range(8)), 0), (6, tuple(range(8)), 1), (0, (), 1), (0, (), 0)])
+def test_the_whole_step_with_experts_or_tokens_left_out(T, absent, n_shared):
+    """What the buffers held before shows nowhere, rows of absent experts included."""
+    E, k, d, f = 8, 2, 256, 128
+    G = Grouped(max(T, 1), E, k, 60 + T, absent=absent)
+    up, upv = matrix(G.n_slots, 2 * f, d, 15)
+    down, downv = matrix(G.n_slots, d, f, 16)
+    cfg = G.cfg.replace(d=d, f=f, n_shared=n_shared)
+    shared = G.shared if n_shared else -1
+    ws = M.workspace(cfg, max(T, 1))  # the grouping lives in it
+    g = H.ctx().group_tokens(cfg, G.dev[0][:T], G.dev[1][:T], T, G.dev[2], G.n_slots, ws)
+    x = values(max(T, 1), d, 17, torch.bfloat16)[:T]
+    (xc, xs), h, (hc, hs) = M.mx4_ffn_buffers(cfg, T)
+    for b in (xc, xs, hc, hs):
+        b.fill_(0xFF)
+    z = torch.full((T * (k + n_shared), d), float("nan"), device="cuda")
+    h.fill_(float("nan"))
+    y = torch.full((T, d), 7.0, device="cuda")
+    H.ctx().expert_ffn_mx4(cfg, x, g, up, down, shared, ((xc, xs), h, (hc, hs)), z)
+    H.ctx().combine(cfg, g, z, x, T, y)
+    assert H.ctx().check_device_status() == M.OK
+    if T == 0:
+        return
+    xv, hv = O.mx4_values(npy(xc), npy(xs)), O.mx4_values(npy(hc), npy(hs))
+    want, size = np.zeros((T, d)), np.zeros((T, d))
+    seen = np.zeros(len(z), bool)
+    for rows, tokens, slot, gate in G.parts(shared=bool(n_shared)):
+        assert_product(h[rows], xv[tokens], upv[slot], HALF[torch.bfloat16], swiglu=True)
+        assert_product(z[rows], hv[rows], downv[slot], HALF[torch.float32], gate=gate)
+        seen[rows] = True
+        np.add.at(want, tokens, npy(z[rows]).astype(np.float64))
+        np.add.at(size, tokens, np.abs(npy(z[rows]).astype(np.float64)))
+    assert np.isnan(npy(z)[~seen]).all()
+    assert np.all(np.abs(npy(y) - want) <= (k + 1) * 2.0 ** -24 * size)
