@@ -18,7 +18,7 @@
 // of a lane group: its maximum, sum and weighted sum are shuffles) and the
 // backward pass writes the gradient once; p is recomputed rather than kept,
 // since an exponential costs less than eight more bytes per logit. Rows: 4 to
-// 32 lanes by E, 1 to 8 float4 per lane, so short rows share a warp. While a row
+// 32 lanes, 1 to 8 float4 per lane, so short rows share a warp. While a row
 // is worked on, the next one's logits, choices and gates are on their way (the
 // choices loaded where they are used: forward 38 against 31 us, backward 55
 // against 48 us at 65521 tokens x 512 experts).
@@ -468,9 +468,9 @@ __global__ void __launch_bounds__(kBThreads)
     // An expert that a row names more than once takes the sum of its parts, in
     // rank order, from each of the lanes that store it.
     bool again = LANES < 32;
-    if (LANES == 32) {
-      const unsigned same = __match_any_sync(0xffffffffu, mine >= 0 ? mine : -1 - lane);
-      again = __any_sync(0xffffffffu, (same & (same - 1)) != 0);
+    if (LANES == 32) {  // the lanes without a choice share one value: a match takes time by their number
+      const unsigned same = __match_any_sync(0xffffffffu, mine);
+      again = __any_sync(0xffffffffu, mine >= 0 && (same & (same - 1)) != 0);
     }
     if (keep) {
       for (int j = sub; j < k; j += LANES) {
@@ -492,28 +492,43 @@ __global__ void __launch_bounds__(kBThreads)
 
 bool rows_vec(const void* p, int E) { return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Lanes of a row and float4 per lane by E, and whether rows are float4s.
+// Lanes of a row and float4 per lane, and whether rows are float4s. A row has
+// few lanes and many values each, so that its shuffles and choices are shared
+// by more rows of the warp: 65521 x 128 forward 22 us with 32 lanes, 14 with 8,
+// backward 33 and 15; 65521 x 64 with 16 and 8 lanes 14.5 and 11.8, 17.5 and
+// 10.7. Where there is at most one row per warp, its time alone counts and more
+// lanes are faster: 300 x 128 backward 3.8 with 32 lanes, 5.2 with 8.
+int lanes_of(const Ctx& ctx, int E, int T) {
+  if (E <= 16) return 4;
+  if (E <= 64) return 8;
+  if (E > 256 || T <= ctx.num_sms * kBWarps) return 32;
+  return E <= 128 ? 8 : 16;
+}
+
 template <typename F>
-cudaError_t by_experts(int E, bool vec, F f) {
+cudaError_t by_experts(int E, int lanes_per_row, bool vec, F f) {
   auto with = [&](auto lanes, auto slots) { return vec ? f(lanes, slots, std::true_type()) : f(lanes, slots, std::false_type()); };
   using std::integral_constant;
-  if (E <= 16) return with(integral_constant<int, 4>(), integral_constant<int, 1>());
-  if (E <= 32) return with(integral_constant<int, 8>(), integral_constant<int, 1>());
-  if (E <= 64) return with(integral_constant<int, 16>(), integral_constant<int, 1>());
+  switch (lanes_per_row) {
+    case 4: return with(integral_constant<int, 4>(), integral_constant<int, 1>());
+    case 8:
+      if (E <= 32) return with(integral_constant<int, 8>(), integral_constant<int, 1>());
+      if (E <= 64) return with(integral_constant<int, 8>(), integral_constant<int, 2>());
+      return with(integral_constant<int, 8>(), integral_constant<int, 4>());
+    case 16: return with(integral_constant<int, 16>(), integral_constant<int, 4>());
+  }
   if (E <= 128) return with(integral_constant<int, 32>(), integral_constant<int, 1>());
   if (E <= 256) return with(integral_constant<int, 32>(), integral_constant<int, 2>());
   if (E <= 512) return with(integral_constant<int, 32>(), integral_constant<int, 4>());
   return with(integral_constant<int, 32>(), integral_constant<int, 8>());
 }
 
-int rows_per_warp(int E) { return E <= 16 ? 8 : E <= 32 ? 4 : E <= 64 ? 2 : 1; }
-
 // One CTA while each of its lane groups has at most kOneCta rows, else up to
 // one per SM.
 constexpr int kOneCta = 4;
 
-int balance_ctas(const Ctx& ctx, int E, int T) {
-  const int per_cta = kBWarps * rows_per_warp(E);
+int balance_ctas(const Ctx& ctx, int lanes, int T) {
+  const int per_cta = kBWarps * (32 / lanes);
   if (T <= per_cta * kOneCta) return 1;
   const int want = (T + per_cta - 1) / per_cta;
   const int most = ctx.num_sms < kBalanceMaxCtas ? ctx.num_sms : kBalanceMaxCtas;
@@ -542,7 +557,7 @@ cudaError_t balance_init(const Ctx& ctx) {
 cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
                            const uint8_t* mask, int T, float* stats, int32_t* counts, float* prob, void* ws,
                            cudaStream_t s) {
-  const int E = c.E, n = T > 0 ? balance_ctas(ctx, E, T) : 1;
+  const int E = c.E, lanes_per_row = lanes_of(ctx, E, T), n = T > 0 ? balance_ctas(ctx, lanes_per_row, T) : 1;
   const BalanceRows R{logits, idx, nullptr, mask, T, E, c.k, ctx.d_status};
   const BalanceOut O{stats, counts, prob};
   char* b = static_cast<char*>(ws);
@@ -555,7 +570,7 @@ cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* 
   P.tok = P.cnt + static_cast<size_t>(kBalanceMaxCtas) * P.pitch;
   P.top = P.tok + kBalanceMaxCtas;
   P.ticket = P.top + 32;
-  const cudaError_t e = by_experts(E, rows_vec(logits, E), [&](auto lanes, auto slots, auto vec) {
+  const cudaError_t e = by_experts(E, lanes_per_row, rows_vec(logits, E), [&](auto lanes, auto slots, auto vec) {
     return launch_dependent(balance_rows_kernel<lanes.value, slots.value, vec.value>, n, kBThreads,
                             static_cast<size_t>(kBWarps) * E * 4, s, R, P, O);
   });
@@ -567,12 +582,12 @@ cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, cons
                                     const float* gate, const uint8_t* mask, int T, const float* stats,
                                     const int32_t* counts, const float* d_loss, const float* d_gate, float* d_logits,
                                     cudaStream_t s) {
-  const int E = c.E;
+  const int E = c.E, lanes_per_row = lanes_of(ctx, E, T);
   const BalanceRows R{logits, idx, gate, mask, T, E, c.k, ctx.d_status};
-  const int per_cta = kBWarps * rows_per_warp(E);
+  const int per_cta = kBWarps * (32 / lanes_per_row);
   const int want = (T + per_cta - 1) / per_cta;
   const int n = want < ctx.num_sms ? want : ctx.num_sms;
-  return by_experts(E, rows_vec(logits, E) && rows_vec(d_logits, E), [&](auto lanes, auto slots, auto vec) {
+  return by_experts(E, lanes_per_row, rows_vec(logits, E) && rows_vec(d_logits, E), [&](auto lanes, auto slots, auto vec) {
     return launch_dependent(balance_backward_kernel<lanes.value, slots.value, vec.value>, n, kBThreads, 0, s, R, stats,
                             counts, d_loss, d_gate, c.renorm != 0, d_logits);
   });

@@ -120,6 +120,25 @@ def test_against_the_oracle(T, E, k, renorm):
     assert H.ctx().check_device_status() == M.OK
 
 
+# enough rows that up to 256 experts share a warp: 8 and 16 lanes a row, choices fewer and more than that
+@pytest.mark.parametrize("T,E,k", [(3600, 65, 32), (4001, 100, 3), (5000, 128, 8), (3700, 130, 20), (4100, 255, 2),
+                                   (3999, 256, 9)])
+@pytest.mark.parametrize("renorm", [True, False], ids=["renorm", "full"])
+def test_many_tokens_of_few_experts(T, E, k, renorm):
+    c = make(T, E, k, seed=T, renorm=renorm, mask=T % 2 == 0, drop=k < 4)
+    c["idx"][5:400:7, 1] = c["idx"][5:400:7, 0]  # named twice
+    c["l"][11] = -1e30
+    c["d_loss"][1] = 0
+    stats, counts, prob, d = Run(c)().out()
+    counted = c["mask"] is None or c["mask"][11] != 0
+    assert np.isinf(stats[1]) == counted
+    if counted:
+        stats = stats.astype(np.float64)
+        stats[1] = O.balance(c["l"], c["idx"], c["mask"])[0][1]
+    check(c, (stats, counts, prob, d))
+    assert H.ctx().check_device_status() == M.OK
+
+
 @pytest.mark.parametrize("T,E", [(37, 16), (1500, 60), (700, 512)])
 def test_losses_alone(T, E):
     c = make(T, E, 2, seed=5, mask=True)
