@@ -24,7 +24,7 @@
 // against 48 us at 65521 tokens x 512 experts).
 //
 // Bound by memory: 65521 x 512 forward 31 us (134 MB, 4.3 TB/s), backward 48 us
-// (268 MB, 5.6 TB/s); at 8192 x 512 (12 and 10 us) by the two launches and the
+// (268 MB, 5.6 TB/s); at 8192 x 512 (12 and 9 us) by the two launches and the
 // two reductions of the forward pass.
 //
 // Sums over tokens: a lane adds its own experts' p over its rows in fp32 (few
