@@ -39,8 +39,12 @@
 namespace moe {
 namespace {
 
-constexpr int kBThreads = 768;  // one CTA per SM leaves 80 registers: a row and the next one's loads
-constexpr int kBWarps = kBThreads / 32;
+// Threads of a CTA, one per SM, by a lane's float4s: 80 registers for a row of up
+// to 4 and the next one's loads, 168 for one of 8 (which 80 would spill: 65521 x
+// 1024 forward 84 us, backward 169).
+constexpr int row_threads(int slots) { return slots > 4 ? 384 : 768; }
+constexpr int row_warps(int slots) { return row_threads(slots) / 32; }
+constexpr int slots_of(int E) { return E > 512 ? 8 : 4; }  // at most
 constexpr int kFinExperts = 32;  // experts of a CTA of the finish
 constexpr int kFinThreads = 256;
 static_assert(kMaxE <= 32 * kFinExperts, "a warp adds up the finish's CTAs");
@@ -141,25 +145,27 @@ struct Partials {
   int32_t* ticket;
 };
 
-// Sum over the CTA, in every thread.
+// Sum over a CTA of WARPS warps, in every thread.
+template <int WARPS>
 __device__ __forceinline__ double block_sum(double v, double* scratch) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = (threadIdx.x & 31) < kBWarps ? scratch[threadIdx.x & 31] : 0.0;
+  v = (threadIdx.x & 31) < WARPS ? scratch[threadIdx.x & 31] : 0.0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
+template <int WARPS>
 __device__ __forceinline__ int block_max(int v, int* scratch) {
   v = __reduce_max_sync(0xffffffffu, v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
   __syncthreads();
-  return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < kBWarps ? scratch[threadIdx.x & 31] : 0);
+  return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < WARPS ? scratch[threadIdx.x & 31] : 0);
 }
 
 // One of a row's choices: choice `sub` in lane `sub` of the row's group.
@@ -225,16 +231,17 @@ __device__ __forceinline__ void write_stats(float* stats, double dot, double z, 
 }
 
 template <int LANES, int SLOTS, bool VEC>
-__global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O) {
+__global__ void __launch_bounds__(row_threads(SLOTS)) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O) {
   using R_ = Row<LANES, SLOTS, VEC>;
-  extern __shared__ float sums[];  // [kBWarps][E]
+  constexpr int kThreads = row_threads(SLOTS), kWarps = row_warps(SLOTS);
+  extern __shared__ float sums[];  // [kWarps][E]
   __shared__ int hist[kMaxE];
-  __shared__ double scratch[kBWarps];
-  __shared__ int iscratch[kBWarps];
+  __shared__ double scratch[kWarps];
+  __shared__ int iscratch[kWarps];
   constexpr int kRows = 32 / LANES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
   const int E = R.E, k = R.k;
-  for (int e = threadIdx.x; e < E; e += kBThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
   grid_dep_wait();
   grid_dep_launch();  // the finish sets up meanwhile; it waits for this grid's end
   __syncthreads();
@@ -244,10 +251,10 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
   for (int i = 0; i < SLOTS * 4; ++i) acc[i] = 0.f;
   double z = 0;
   int n = 0;
-  const int stride = gridDim.x * kBWarps * kRows;
-  Walk<LANES, SLOTS, VEC> walk(R, nullptr, (blockIdx.x * kBWarps + warp) * kRows + lane / LANES, stride, sub);
+  const int stride = gridDim.x * kWarps * kRows;
+  Walk<LANES, SLOTS, VEC> walk(R, nullptr, (blockIdx.x * kWarps + warp) * kRows + lane / LANES, stride, sub);
   // every lane of a warp makes the same number of turns: the shuffles are warp-wide
-  for (int t0 = (blockIdx.x * kBWarps + warp) * kRows; t0 < R.T; t0 += stride) {
+  for (int t0 = (blockIdx.x * kWarps + warp) * kRows; t0 < R.T; t0 += stride) {
     walk.step();
     const int t = walk.t;
     R_& row = walk.row;
@@ -278,12 +285,12 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
     const int e = R_::expert(i / 4, sub) + i % 4;
     if (lane < LANES && e < E) sums[warp * E + e] = acc[i];
   }
-  z = block_sum(z, scratch);  // its barriers also publish sums and hist
-  n = static_cast<int>(block_sum(static_cast<double>(n), scratch));
+  z = block_sum<kWarps>(z, scratch);  // its barriers also publish sums and hist
+  n = static_cast<int>(block_sum<kWarps>(static_cast<double>(n), scratch));
   if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e < E; e += kBThreads) {
+    for (int e = threadIdx.x; e < E; e += kThreads) {
       float s = 0.f;
-      for (int w = 0; w < kBWarps; ++w) s += sums[w * E + e];
+      for (int w = 0; w < kWarps; ++w) s += sums[w * E + e];
       P.sum[blockIdx.x * P.pitch + e] = s;
       P.cnt[blockIdx.x * P.pitch + e] = hist[e];
     }
@@ -297,16 +304,16 @@ __global__ void __launch_bounds__(kBThreads) balance_rows_kernel(BalanceRows R, 
   // all rows were this CTA's: finish here
   double dot = 0;
   int top = 0;
-  for (int e = threadIdx.x; e < E; e += kBThreads) {
+  for (int e = threadIdx.x; e < E; e += kThreads) {
     double s = 0;
-    for (int w = 0; w < kBWarps; ++w) s += sums[w * E + e];
+    for (int w = 0; w < kWarps; ++w) s += sums[w * E + e];
     dot += s * hist[e];
     top = max(top, hist[e]);
     O.prob[e] = static_cast<float>(s / max(n, 1));
     O.counts[e] = hist[e];
   }
-  dot = block_sum(dot, scratch);
-  top = block_max(top, iscratch);
+  dot = block_sum<kWarps>(dot, scratch);
+  top = block_max<kWarps>(top, iscratch);
   if (threadIdx.x == 0) write_stats(O.stats, dot, z, n, top, E, k);
 }
 
@@ -395,12 +402,12 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(Partials P,
 }
 
 template <int LANES, int SLOTS, bool VEC>
-__global__ void __launch_bounds__(kBThreads)
+__global__ void __launch_bounds__(row_threads(SLOTS))
     balance_backward_kernel(BalanceRows R, const float* stats, const int32_t* counts, const float* d_loss,
                             const float* d_gate, bool renorm,
                             float* __restrict__ d_logits) {
   using R_ = Row<LANES, SLOTS, VEC>;
-  constexpr int kRows = 32 / LANES;
+  constexpr int kRows = 32 / LANES, kWarps = row_warps(SLOTS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
   const int E = R.E, k = R.k;
   grid_dep_wait();
@@ -413,9 +420,9 @@ __global__ void __launch_bounds__(kBThreads)
     const int e = R_::expert(i / 4, sub) + i % 4;
     c[i] = e < E ? ca * ld_plain(counts + e) : 0.f;
   }
-  const int stride = gridDim.x * kBWarps * kRows;
-  Walk<LANES, SLOTS, VEC> walk(R, d_gate, (blockIdx.x * kBWarps + warp) * kRows + lane / LANES, stride, sub);
-  for (int t0 = (blockIdx.x * kBWarps + warp) * kRows; t0 < R.T; t0 += stride) {
+  const int stride = gridDim.x * kWarps * kRows;
+  Walk<LANES, SLOTS, VEC> walk(R, d_gate, (blockIdx.x * kWarps + warp) * kRows + lane / LANES, stride, sub);
+  for (int t0 = (blockIdx.x * kWarps + warp) * kRows; t0 < R.T; t0 += stride) {
     walk.step();
     const bool live = walk.t < R.T, in = walk.in != 0;
     const size_t at = live ? walk.t : 0;
@@ -501,7 +508,7 @@ bool rows_vec(const void* p, int E) { return E % 4 == 0 && reinterpret_cast<uint
 int lanes_of(const Ctx& ctx, int E, int T) {
   if (E <= 16) return 4;
   if (E <= 64) return 8;
-  if (E > 256 || T <= ctx.num_sms * kBWarps) return 32;
+  if (E > 256 || T <= ctx.num_sms * row_warps(slots_of(E))) return 32;
   return E <= 128 ? 8 : 16;
 }
 
@@ -527,8 +534,8 @@ cudaError_t by_experts(int E, int lanes_per_row, bool vec, F f) {
 // one per SM.
 constexpr int kOneCta = 4;
 
-int balance_ctas(const Ctx& ctx, int lanes, int T) {
-  const int per_cta = kBWarps * (32 / lanes);
+int balance_ctas(const Ctx& ctx, int E, int lanes, int T) {
+  const int per_cta = row_warps(slots_of(E)) * (32 / lanes);
   if (T <= per_cta * kOneCta) return 1;
   const int want = (T + per_cta - 1) / per_cta;
   const int most = ctx.num_sms < kBalanceMaxCtas ? ctx.num_sms : kBalanceMaxCtas;
@@ -548,7 +555,7 @@ cudaError_t balance_init(const Ctx& ctx) {
                         reinterpret_cast<const void*>(balance_rows_kernel<32, 8, true>),
                         reinterpret_cast<const void*>(balance_rows_kernel<32, 8, false>)};
   for (const void* fn : fns) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kBWarps * kMaxE * 4);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, row_warps(4) * 512 * 4);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -557,7 +564,7 @@ cudaError_t balance_init(const Ctx& ctx) {
 cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
                            const uint8_t* mask, int T, float* stats, int32_t* counts, float* prob, void* ws,
                            cudaStream_t s) {
-  const int E = c.E, lanes_per_row = lanes_of(ctx, E, T), n = T > 0 ? balance_ctas(ctx, lanes_per_row, T) : 1;
+  const int E = c.E, lanes_per_row = lanes_of(ctx, E, T), n = T > 0 ? balance_ctas(ctx, E, lanes_per_row, T) : 1;
   const BalanceRows R{logits, idx, nullptr, mask, T, E, c.k, ctx.d_status};
   const BalanceOut O{stats, counts, prob};
   char* b = static_cast<char*>(ws);
@@ -571,8 +578,8 @@ cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* 
   P.top = P.tok + kBalanceMaxCtas;
   P.ticket = P.top + 32;
   const cudaError_t e = by_experts(E, lanes_per_row, rows_vec(logits, E), [&](auto lanes, auto slots, auto vec) {
-    return launch_dependent(balance_rows_kernel<lanes.value, slots.value, vec.value>, n, kBThreads,
-                            static_cast<size_t>(kBWarps) * E * 4, s, R, P, O);
+    return launch_dependent(balance_rows_kernel<lanes.value, slots.value, vec.value>, n, row_threads(slots.value),
+                            static_cast<size_t>(row_warps(slots.value)) * E * 4, s, R, P, O);
   });
   if (e != cudaSuccess || n == 1) return e;
   return launch_dependent(balance_finish_kernel, (E + kFinExperts - 1) / kFinExperts, kFinThreads, 0, s, P, O, n, E, c.k);
@@ -584,11 +591,11 @@ cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, cons
                                     cudaStream_t s) {
   const int E = c.E, lanes_per_row = lanes_of(ctx, E, T);
   const BalanceRows R{logits, idx, gate, mask, T, E, c.k, ctx.d_status};
-  const int per_cta = kBWarps * (32 / lanes_per_row);
+  const int per_cta = row_warps(slots_of(E)) * (32 / lanes_per_row);
   const int want = (T + per_cta - 1) / per_cta;
   const int n = want < ctx.num_sms ? want : ctx.num_sms;
   return by_experts(E, lanes_per_row, rows_vec(logits, E) && rows_vec(d_logits, E), [&](auto lanes, auto slots, auto vec) {
-    return launch_dependent(balance_backward_kernel<lanes.value, slots.value, vec.value>, n, kBThreads, 0, s, R, stats,
+    return launch_dependent(balance_backward_kernel<lanes.value, slots.value, vec.value>, n, row_threads(slots.value), 0, s, R, stats,
                             counts, d_loss, d_gate, c.renorm != 0, d_logits);
   });
 }
