@@ -40,11 +40,13 @@ namespace moe {
 namespace {
 
 // Threads of a CTA, one per SM, by a lane's float4s: 80 registers for a row of up
-// to 4 and the next one's loads, 168 for one of 8 (which 80 would spill: 65521 x
-// 1024 forward 84 us, backward 169).
-constexpr int row_threads(int slots) { return slots > 4 ? 384 : 768; }
+// to 4 and the next one's loads, 128 for one of 6 and 168 for one of 8 (which 80
+// would spill: 65521 x
+// 1024 forward 86 us, backward 168, now 60 and 89; 65521 x 768 74 and 130, with 8
+// slots 60 and 75, with 6 41 and 68).
+constexpr int row_threads(int slots) { return slots > 6 ? 384 : slots > 4 ? 512 : 768; }
 constexpr int row_warps(int slots) { return row_threads(slots) / 32; }
-constexpr int slots_of(int E) { return E > 512 ? 8 : 4; }  // at most
+constexpr int slots_of(int E) { return E > 768 ? 8 : E > 512 ? 6 : 4; }  // at most
 constexpr int kFinExperts = 32;  // experts of a CTA of the finish
 constexpr int kFinThreads = 256;
 static_assert(kMaxE <= 32 * kFinExperts, "a warp adds up the finish's CTAs");
@@ -527,6 +529,7 @@ cudaError_t by_experts(int E, int lanes_per_row, bool vec, F f) {
   if (E <= 128) return with(integral_constant<int, 32>(), integral_constant<int, 1>());
   if (E <= 256) return with(integral_constant<int, 32>(), integral_constant<int, 2>());
   if (E <= 512) return with(integral_constant<int, 32>(), integral_constant<int, 4>());
+  if (E <= 768) return with(integral_constant<int, 32>(), integral_constant<int, 6>());
   return with(integral_constant<int, 32>(), integral_constant<int, 8>());
 }
 
@@ -550,8 +553,10 @@ size_t balance_ws_bytes(int E) {
 
 cudaError_t balance_init(const Ctx& ctx) {
   (void)ctx;
-  const void* fns[4] = {reinterpret_cast<const void*>(balance_rows_kernel<32, 4, true>),
+  const void* fns[6] = {reinterpret_cast<const void*>(balance_rows_kernel<32, 4, true>),
                         reinterpret_cast<const void*>(balance_rows_kernel<32, 4, false>),
+                        reinterpret_cast<const void*>(balance_rows_kernel<32, 6, true>),
+                        reinterpret_cast<const void*>(balance_rows_kernel<32, 6, false>),
                         reinterpret_cast<const void*>(balance_rows_kernel<32, 8, true>),
                         reinterpret_cast<const void*>(balance_rows_kernel<32, 8, false>)};
   for (const void* fn : fns) {
