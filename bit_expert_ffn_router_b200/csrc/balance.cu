@@ -23,12 +23,13 @@
 // choices loaded where they are used: forward 38 against 31 us, backward 55
 // against 48 us at 65521 tokens x 512 experts).
 //
-// Bound by memory: 65521 x 512 forward 31 us (134 MB, 4.3 TB/s), backward 48 us
-// (268 MB, 5.6 TB/s); at 8192 x 512 (12 and 9 us) by the two launches and the
+// Bound by memory, the forward pass by its instructions too (65% of the issue
+// slots): 65521 x 512 forward 31 us (134 MB, 4.3 TB/s), backward 48 us (268 MB,
+// 5.6 TB/s), x 1024 53 and 89 us (5.1, 6.0 TB/s); at 8192 x 512 (12 and 9 us) by the two launches and the
 // two reductions of the forward pass.
 //
-// Sums over tokens: a lane adds its own experts' p over its rows in fp32 (few
-// dozen of them), the CTA adds its lane groups in a fixed order, and the finish
+// Sums over tokens: a lane adds its own experts' p over its rows in fp32 (T /
+// 3552 of them at 512 experts), the CTA adds its lane groups in a fixed order, and the finish
 // adds the CTAs' partial sums in fp64, in a fixed order too: results do not
 // depend on the timing. The counts are integer atomics in shared memory.
 #include <type_traits>
@@ -40,12 +41,12 @@ namespace moe {
 namespace {
 
 // Threads of a CTA, one per SM, by a lane's float4s: 80 registers for a row of up
-// to 4 and the next one's loads, 128 for one of 6 and 168 for one of 8 (which 80
-// would spill: 65521 x
-// 1024 forward 86 us, backward 168, now 60 and 89; 65521 x 768 74 and 130, with 8
-// slots 60 and 75, with 6 41 and 68).
-constexpr int row_threads(int slots) { return slots > 6 ? 384 : slots > 4 ? 512 : 768; }
-constexpr int row_warps(int slots) { return row_threads(slots) / 32; }
+// to 4 and the next one's loads, 128 for one of 6, 144 (forward) or 168 for one
+// of 8. 65521 rows with 768 threads, which spill, then with these:
+// 1024 forward 86 and 53 us (384 threads: 61), backward 168 and 89 (448: 96); 768
+// forward 74 and 41 (8 slots: 60), backward 130 and 68 (75).
+constexpr int row_threads(int slots, bool forward) { return slots > 6 ? (forward ? 448 : 384) : slots > 4 ? 512 : 768; }
+constexpr int row_warps(int slots, bool forward) { return row_threads(slots, forward) / 32; }
 constexpr int slots_of(int E) { return E > 768 ? 8 : E > 512 ? 6 : 4; }  // at most
 constexpr int kFinExperts = 32;  // experts of a CTA of the finish
 constexpr int kFinThreads = 256;
@@ -233,9 +234,9 @@ __device__ __forceinline__ void write_stats(float* stats, double dot, double z, 
 }
 
 template <int LANES, int SLOTS, bool VEC>
-__global__ void __launch_bounds__(row_threads(SLOTS)) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O) {
+__global__ void __launch_bounds__(row_threads(SLOTS, true)) balance_rows_kernel(BalanceRows R, Partials P, BalanceOut O) {
   using R_ = Row<LANES, SLOTS, VEC>;
-  constexpr int kThreads = row_threads(SLOTS), kWarps = row_warps(SLOTS);
+  constexpr int kThreads = row_threads(SLOTS, true), kWarps = row_warps(SLOTS, true);
   extern __shared__ float sums[];  // [kWarps][E]
   __shared__ int hist[kMaxE];
   __shared__ double scratch[kWarps];
@@ -404,12 +405,12 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(Partials P,
 }
 
 template <int LANES, int SLOTS, bool VEC>
-__global__ void __launch_bounds__(row_threads(SLOTS))
+__global__ void __launch_bounds__(row_threads(SLOTS, false))
     balance_backward_kernel(BalanceRows R, const float* stats, const int32_t* counts, const float* d_loss,
                             const float* d_gate, bool renorm,
                             float* __restrict__ d_logits) {
   using R_ = Row<LANES, SLOTS, VEC>;
-  constexpr int kRows = 32 / LANES, kWarps = row_warps(SLOTS);
+  constexpr int kRows = 32 / LANES, kWarps = row_warps(SLOTS, false);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
   const int E = R.E, k = R.k;
   grid_dep_wait();
@@ -510,7 +511,7 @@ bool rows_vec(const void* p, int E) { return E % 4 == 0 && reinterpret_cast<uint
 int lanes_of(const Ctx& ctx, int E, int T) {
   if (E <= 16) return 4;
   if (E <= 64) return 8;
-  if (E > 256 || T <= ctx.num_sms * row_warps(slots_of(E))) return 32;
+  if (E > 256 || T <= ctx.num_sms * row_warps(slots_of(E), true)) return 32;
   return E <= 128 ? 8 : 16;
 }
 
@@ -538,7 +539,7 @@ cudaError_t by_experts(int E, int lanes_per_row, bool vec, F f) {
 constexpr int kOneCta = 4;
 
 int balance_ctas(const Ctx& ctx, int E, int lanes, int T) {
-  const int per_cta = row_warps(slots_of(E)) * (32 / lanes);
+  const int per_cta = row_warps(slots_of(E), true) * (32 / lanes);
   if (T <= per_cta * kOneCta) return 1;
   const int want = (T + per_cta - 1) / per_cta;
   const int most = ctx.num_sms < kBalanceMaxCtas ? ctx.num_sms : kBalanceMaxCtas;
@@ -560,7 +561,8 @@ cudaError_t balance_init(const Ctx& ctx) {
                         reinterpret_cast<const void*>(balance_rows_kernel<32, 8, true>),
                         reinterpret_cast<const void*>(balance_rows_kernel<32, 8, false>)};
   for (const void* fn : fns) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, row_warps(4) * 512 * 4);
+    const cudaError_t e =
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, row_warps(8, true) * kMaxE * 4);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -583,8 +585,8 @@ cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* 
   P.top = P.tok + kBalanceMaxCtas;
   P.ticket = P.top + 32;
   const cudaError_t e = by_experts(E, lanes_per_row, rows_vec(logits, E), [&](auto lanes, auto slots, auto vec) {
-    return launch_dependent(balance_rows_kernel<lanes.value, slots.value, vec.value>, n, row_threads(slots.value),
-                            static_cast<size_t>(row_warps(slots.value)) * E * 4, s, R, P, O);
+    return launch_dependent(balance_rows_kernel<lanes.value, slots.value, vec.value>, n, row_threads(slots.value, true),
+                            static_cast<size_t>(row_warps(slots.value, true)) * E * 4, s, R, P, O);
   });
   if (e != cudaSuccess || n == 1) return e;
   return launch_dependent(balance_finish_kernel, (E + kFinExperts - 1) / kFinExperts, kFinThreads, 0, s, P, O, n, E, c.k);
@@ -596,12 +598,13 @@ cudaError_t launch_balance_backward(const Ctx& ctx, const moe_layer_cfg& c, cons
                                     cudaStream_t s) {
   const int E = c.E, lanes_per_row = lanes_of(ctx, E, T);
   const BalanceRows R{logits, idx, gate, mask, T, E, c.k, ctx.d_status};
-  const int per_cta = row_warps(slots_of(E)) * (32 / lanes_per_row);
+  const int per_cta = row_warps(slots_of(E), false) * (32 / lanes_per_row);
   const int want = (T + per_cta - 1) / per_cta;
   const int n = want < ctx.num_sms ? want : ctx.num_sms;
   return by_experts(E, lanes_per_row, rows_vec(logits, E) && rows_vec(d_logits, E), [&](auto lanes, auto slots, auto vec) {
-    return launch_dependent(balance_backward_kernel<lanes.value, slots.value, vec.value>, n, row_threads(slots.value), 0, s, R, stats,
-                            counts, d_loss, d_gate, c.renorm != 0, d_logits);
+    return launch_dependent(balance_backward_kernel<lanes.value, slots.value, vec.value>, n,
+                            row_threads(slots.value, false), 0, s, R, stats, counts, d_loss, d_gate, c.renorm != 0,
+                            d_logits);
   });
 }
 

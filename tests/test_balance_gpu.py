@@ -109,7 +109,7 @@ def check(c, got, d_gate=True):
 
 SHAPES = [(1, 1, 1), (1, 8, 2), (3, 7, 7), (37, 16, 2), (64, 17, 4), (65, 32, 3), (129, 33, 5), (200, 64, 8), (31, 100, 9),
           (300, 128, 8), (77, 130, 10), (257, 256, 6), (8, 512, 10), (64, 512, 10), (65, 512, 10), (1000, 512, 10),
-          (130, 513, 32), (70, 1023, 11), (90, 1024, 32)]
+          (130, 513, 32), (70, 1023, 11), (90, 1024, 32), (1900, 768, 8), (1901, 767, 5), (1800, 1000, 12)]
 
 
 @pytest.mark.parametrize("T,E,k", SHAPES)
