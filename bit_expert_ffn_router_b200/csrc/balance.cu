@@ -189,7 +189,7 @@ struct Choice {
 // The rows of a lane group, first + stride * i: the row at hand, the next one's
 // logits and choices on their way, and the flag (the mask's byte; 0 past the
 // end) of the one after it. A row that does not count is not read: row 0
-// stands in.
+// stands in (the launchers see to it that there is one).
 template <int LANES, int SLOTS, bool VEC>
 struct Walk {
   const BalanceRows& R;
@@ -582,7 +582,13 @@ cudaError_t balance_init(const Ctx& ctx) {
 cudaError_t launch_balance(const Ctx& ctx, const moe_layer_cfg& c, const float* logits, const int32_t* idx,
                            const uint8_t* mask, int T, float* stats, int32_t* counts, float* prob, void* ws,
                            cudaStream_t s) {
-  const int E = c.E, lanes_per_row = lanes_of(ctx, E, T), n = T > 0 ? balance_ctas(ctx, E, lanes_per_row, T) : 1;
+  const int E = c.E;
+  if (T == 0) {  // no row 0 to stand in for the rows that do not count: logits and idx may be null
+    cudaError_t e = cudaMemsetAsync(stats, 0, 4 * sizeof(float), s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(counts, 0, E * sizeof(int32_t), s);
+    return e == cudaSuccess ? cudaMemsetAsync(prob, 0, E * sizeof(float), s) : e;
+  }
+  const int lanes_per_row = lanes_of(ctx, E, T), n = balance_ctas(ctx, E, lanes_per_row, T);
   const BalanceRows R{logits, idx, nullptr, mask, T, E, c.k, ctx.d_status};
   const BalanceOut O{stats, counts, prob};
   char* b = static_cast<char*>(ws);

@@ -255,6 +255,28 @@ def test_no_tokens():
     assert not stats.any() and not counts.any() and not prob.any() and (d == 7).all()
 
 
+@pytest.mark.parametrize("E,k", [(16, 2), (13, 3), (512, 10), (1024, 32)])
+@pytest.mark.parametrize("mask", [False, True])
+def test_empty_tensors(E, k, mask):
+    """A batch without tokens: tensors of no elements have the null address."""
+    c = make(0, E, k, seed=E, mask=mask)
+    r = Run(c)
+    assert r.T == 0 and r.l.data_ptr() == 0 and r.idx.data_ptr() == 0
+    assert not any(a.any() for a in r().out())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            r(stream=s)
+        for t in (r.stats, r.counts, r.prob):
+            t.fill_(7)
+        g.replay()
+        s.synchronize()
+    assert not any(a.any() for a in r.out())
+    assert H.ctx().check_device_status() == M.OK
+
+
 def test_long_batch_equal_bits_and_captured_replays():
     c = make(9001, 512, 10, seed=15, mask=True)
     r = Run(c)
