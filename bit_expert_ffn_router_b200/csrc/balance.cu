@@ -443,7 +443,9 @@ __global__ void __launch_bounds__(row_threads(SLOTS, false))
     const float* tg = R.gate + at * k;
     const float* td = d_gate + at * k;
     const int mine = walk.choice.e;
-    const float g = walk.choice.gate, gd = g * walk.choice.d_gate;
+    // a choice that names no expert takes no part, whatever its gate holds
+    const bool named = static_cast<unsigned>(mine) < static_cast<unsigned>(E);
+    const float g = walk.choice.gate, gd = named ? g * walk.choice.d_gate : 0.f;
     float m;
     const float s = row.exp_sum(m);
     const bool keep = in && s != 0.f;
@@ -457,7 +459,10 @@ __global__ void __launch_bounds__(row_threads(SLOTS, false))
     if (d_gate != nullptr) {
       gs = gd;
       if (LANES < 32)
-        for (int j = sub + LANES; j < k; j += LANES) gs = fmaf(ld_plain(tg + j), ld_plain(td + j), gs);
+        for (int j = sub + LANES; j < k; j += LANES) {
+          const float more = fmaf(ld_plain(tg + j), ld_plain(td + j), gs);
+          if (static_cast<unsigned>(ld_plain(ti + j)) < static_cast<unsigned>(E)) gs = more;
+        }
       gs = group_sum(gs, LANES);
     }
     // every expert: p * (c_e + base); a z gradient of 0 leaves an infinite lse out

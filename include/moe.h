@@ -411,8 +411,9 @@ MOE_API moe_status moe_layer_forward_static(moe_ctx* ctx, const moe_layer_cfg* c
  * d_gate: [T, k], or NULL for the losses alone (gate may then be NULL);
  * stats, counts: from moe_balance_loss on the same logits, idx and mask. Rows
  * that do not count get 0, their gates' part included. An expert that a row
- * names twice takes both parts; an idx outside [0, E) none. d_logits must not
- * overlap the inputs. */
+ * names twice takes both parts. A choice whose idx is outside [0, E) takes no
+ * part: the sum over d_gate * gate leaves it out, and its gate and d_gate may
+ * hold anything. d_logits must not overlap the inputs. */
 MOE_API size_t moe_balance_workspace_bytes(const moe_layer_cfg* cfg);
 MOE_API moe_status moe_balance_loss(moe_ctx* ctx, const moe_layer_cfg* cfg, const float* logits, const int32_t* idx,
                                     const uint8_t* mask, int T, float* stats, int32_t* counts, float* prob, void* ws,

@@ -58,8 +58,9 @@ def balance_grad(logits, idx, gate, mask, d_loss, d_gate, renorm):
         size[t] = p * (abs(a) * (counts + (counts * p).sum()) + abs(z))
         if d_gate is not None:
             g, dg = gate[t].astype(np.float64), d_gate[t].astype(np.float64)
-            mean = (g * dg).sum()
-            mag = (g * abs(dg)).sum()
+            ok = (idx[t] >= 0) & (idx[t] < E)  # a choice that names no expert takes no part
+            mean = (g * dg)[ok].sum()
+            mag = (g * abs(dg))[ok].sum()
             if not renorm:
                 out[t] -= p * mean
                 size[t] += p * mag

@@ -227,6 +227,22 @@ def test_bad_choice_is_reported_and_counts_nowhere(E):
     assert H.ctx().last_device_error_detail() in (7, 16)
 
 
+@pytest.mark.parametrize("T,E,k", [(40, 16, 2), (40, 16, 11), (300, 61, 20), (3900, 100, 20), (3700, 256, 17), (90, 512, 10),
+                                   (60, 1024, 32)])
+@pytest.mark.parametrize("renorm", [True, False], ids=["renorm", "full"])
+def test_a_bad_choice_takes_no_part_in_the_gradient(T, E, k, renorm):
+    """Its gate and d_gate are not looked at, and the row's other choices and experts go on without it."""
+    c = make(T, E, k, seed=16, renorm=renorm)
+    rng = np.random.default_rng(17)
+    for bad, g, dg in ((E, 0.5, 1.0), (-1, np.nan, 1.0), (2 ** 31 - 1, 0.25, np.inf), (-2 ** 31, np.inf, np.nan)):
+        for t in rng.integers(0, T, size=9):
+            j = int(rng.integers(0, k))
+            c["idx"][t, j], c["gate"][t, j], c["d_gate"][t, j] = bad, g, dg
+    c["idx"][3], c["gate"][3], c["d_gate"][3] = -1, np.nan, np.nan  # a row without a choice
+    check(c, Run(c)().out())
+    assert H.ctx().check_device_status() == M.EDEVICE
+
+
 @pytest.mark.parametrize("E,k", [(16, 4), (512, 10)])
 def test_an_expert_named_twice_takes_both_parts(E, k):
     c = make(33, E, k, seed=12)

@@ -50,6 +50,35 @@ def test_gradient_against_differences(renorm):
             assert abs(num - d[t, i]) < 1e-7
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+def test_a_choice_that_names_no_expert_takes_no_part(renorm):
+    """Its gate and gradient are not looked at; the others' gradient is that of the sum over the named choices, whose
+    softmax may have a constant beside them."""
+    rng = np.random.default_rng(4)
+    E, k, beside = 6, 3, 0.8
+    l, dg, idx = rng.normal(size=(1, E)), rng.normal(size=(1, k)), np.array([[4, E, 1]])
+
+    def gates(l):
+        e = np.exp(l[0])
+        return e[[4, 1]] / (e[[4, 1]].sum() + beside if renorm else e.sum())
+
+    g = gates(l)
+    gate = np.array([[g[0], np.nan, g[1]]])
+    d, size = O.balance_grad(l, idx, gate, None, [0, 0], dg, renorm)
+    dg[0, 1] = np.inf
+    again, _ = O.balance_grad(l, idx, gate, None, [0, 0], dg, renorm)
+    assert np.array_equal(d, again) and np.isfinite(size).all()
+    h = 1e-6
+    for i in range(E):
+        a, b = l.copy(), l.copy()
+        a[0, i] += h
+        b[0, i] -= h
+        num = ((gates(a) - gates(b)) * dg[0, [0, 2]]).sum() / (2 * h)
+        if renorm and i not in (4, 1):
+            assert d[0, i] == 0
+        assert abs(num - d[0, i]) < 1e-8
+
+
 def test_quantised_values_by_hand():
     x = np.zeros((1, 64))
     x[0, :12] = [4, 0.25, 0.26, -0.75, 1.25, 1.75, 2.5, 3.5, 5, -5.01, 7.9, -0.1]
