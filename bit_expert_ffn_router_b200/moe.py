@@ -51,8 +51,17 @@ class Routing(ctypes.Structure):
                 ("grouping", Grouping)]
 
 
+class _WithRef:
+    """Room for a configuration's C structure beside its fields, not among them: vars(), copies and pickles hold the
+    fields alone."""
+    __slots__ = ("_ref",)
+
+    def __getstate__(self):
+        return self.__dict__
+
+
 @dataclasses.dataclass(frozen=True)
-class LayerCfg:
+class LayerCfg(_WithRef):
     d: int
     f: int
     E: int
@@ -67,12 +76,16 @@ class LayerCfg:
     hot_slots: int = 0
 
     def c(self) -> _Cfg:
-        """The C structure (built once; the library only reads it)."""
-        c = self.__dict__.get("_struct")
-        if c is None:
-            c = _Cfg(*(getattr(self, f.name) for f in dataclasses.fields(self)))
-            object.__setattr__(self, "_struct", c)
-        return c
+        """A C structure of these fields, the caller's own."""
+        return _Cfg(*(getattr(self, f.name) for f in dataclasses.fields(self)))
+
+    def ref(self):
+        """A pointer argument to a structure that is built once (the library only reads it)."""
+        try:
+            return self._ref
+        except AttributeError:
+            object.__setattr__(self, "_ref", ctypes.byref(self.c()))
+            return self._ref
 
     def replace(self, **kw) -> "LayerCfg":
         return dataclasses.replace(self, **kw)
@@ -162,12 +175,12 @@ def _check(status: int, what: str) -> None:
 
 def expert_layout(cfg: LayerCfg) -> dict:
     lay = _Layout()
-    _check(load_library().moe_expert_layout_get(ctypes.byref(cfg.c()), ctypes.byref(lay)), "moe_expert_layout_get")
+    _check(load_library().moe_expert_layout_get(cfg.ref(), ctypes.byref(lay)), "moe_expert_layout_get")
     return {n: getattr(lay, n) for n, _ in _Layout._fields_}
 
 
 def workspace_bytes(cfg: LayerCfg, T: int) -> int:
-    return int(load_library().moe_workspace_bytes(ctypes.byref(cfg.c()), T))
+    return int(load_library().moe_workspace_bytes(cfg.ref(), T))
 
 
 def _ptr(t):
@@ -204,19 +217,19 @@ class Context:
 
     # -- raw entry points (status codes returned, not raised) --------------------
     def router_topk_status(self, cfg, x, w_router, bias, T, logits, idx, gate, stream=None):
-        return self.lib.moe_router_topk(self.h, ctypes.byref(cfg.c()), _ptr(x), _ptr(w_router), _ptr(bias), T,
+        return self.lib.moe_router_topk(self.h, cfg.ref(), _ptr(x), _ptr(w_router), _ptr(bias), T,
                                         _ptr(logits), _ptr(idx), _ptr(gate), _stream(stream))
 
     def layer_forward_status(self, cfg, x, T, w_router, bias, slot_of, n_slots, pool, stride, shared, ws, y,
                              stream=None):
-        return self.lib.moe_layer_forward(self.h, ctypes.byref(cfg.c()), _ptr(x), T, _ptr(w_router), _ptr(bias),
+        return self.lib.moe_layer_forward(self.h, cfg.ref(), _ptr(x), T, _ptr(w_router), _ptr(bias),
                                           _ptr(slot_of), n_slots, _ptr(pool), stride, _ptr(shared), _ptr(ws),
                                           0 if ws is None else ws.numel() * ws.element_size(), _ptr(y),
                                           _stream(stream))
 
     def stack_forward_status(self, cfg, L, x, T, w_router, bias, slot_of, n_slots, pool, stride, shared, ws, y,
                              stream=None):
-        return self.lib.moe_stack_forward(self.h, ctypes.byref(cfg.c()), L, _ptr(x), T, _ptr(w_router), _ptr(bias),
+        return self.lib.moe_stack_forward(self.h, cfg.ref(), L, _ptr(x), T, _ptr(w_router), _ptr(bias),
                                           _ptr(slot_of), n_slots, _ptr(pool), stride, _ptr(shared), _ptr(ws),
                                           0 if ws is None else ws.numel() * ws.element_size(), _ptr(y),
                                           _stream(stream))
@@ -230,7 +243,7 @@ class Context:
     def layer_forward_static_status(self, cfg, x, T, w_router, bias, slot_of, n_slots, pool, stride, shared, y,
                                     stream=None):
         """moe_layer_forward with the library's static scratch (no workspace argument)."""
-        return self.lib.moe_layer_forward_static(self.h, ctypes.byref(cfg.c()), _ptr(x), T, _ptr(w_router),
+        return self.lib.moe_layer_forward_static(self.h, cfg.ref(), _ptr(x), T, _ptr(w_router),
                                                  _ptr(bias), _ptr(slot_of), n_slots, _ptr(pool), stride,
                                                  _ptr(shared), _ptr(y), _stream(stream))
 
@@ -239,24 +252,24 @@ class Context:
         _check(self.router_topk_status(cfg, x, w_router, bias, T, logits, idx, gate, stream), "moe_router_topk")
 
     def topk(self, cfg, logits, T, idx, gate, stream=None):
-        _check(self.lib.moe_topk(self.h, ctypes.byref(cfg.c()), _ptr(logits), T, _ptr(idx), _ptr(gate),
+        _check(self.lib.moe_topk(self.h, cfg.ref(), _ptr(logits), T, _ptr(idx), _ptr(gate),
                                  _stream(stream)), "moe_topk")
 
     def group_tokens(self, cfg, idx, gate, T, slot_of, n_slots, ws, stream=None) -> Grouping:
         g = Grouping()
-        _check(self.lib.moe_group_tokens(self.h, ctypes.byref(cfg.c()), _ptr(idx), _ptr(gate), T, _ptr(slot_of),
+        _check(self.lib.moe_group_tokens(self.h, cfg.ref(), _ptr(idx), _ptr(gate), T, _ptr(slot_of),
                                          n_slots, _ptr(ws), ws.numel() * ws.element_size(), ctypes.byref(g),
                                          _stream(stream)), "moe_group_tokens")
         return g
 
     def expert_ffn(self, cfg, x, grouping, pool, stride, shared, ws, z_rows=None, y=None, stream=None):
         fn = self.lib.moe_expert_ffn_q2 if cfg.bits == 2 else self.lib.moe_expert_ffn_q3
-        _check(fn(self.h, ctypes.byref(cfg.c()), _ptr(x), ctypes.byref(grouping), _ptr(pool), stride, _ptr(shared),
+        _check(fn(self.h, cfg.ref(), _ptr(x), ctypes.byref(grouping), _ptr(pool), stride, _ptr(shared),
                   _ptr(ws), ws.numel() * ws.element_size(), _ptr(z_rows), _ptr(y), _stream(stream)),
                f"moe_expert_ffn_q{cfg.bits}")
 
     def combine(self, cfg, grouping, z_rows, x, T, y, stream=None):
-        _check(self.lib.moe_combine(self.h, ctypes.byref(cfg.c()), ctypes.byref(grouping), _ptr(z_rows), _ptr(x),
+        _check(self.lib.moe_combine(self.h, cfg.ref(), ctypes.byref(grouping), _ptr(z_rows), _ptr(x),
                                     T, _ptr(y), _stream(stream)), "moe_combine")
 
     def layer_forward(self, cfg, x, T, w_router, bias, slot_of, n_slots, pool, stride, shared, ws, y,
@@ -270,7 +283,7 @@ class Context:
         return PreparedLayer(self, cfg, T, w_router, bias, slot_of, n_slots, pool, stride, shared, ws, stream)
 
     def usage_count_status(self, cfg, L, T, ws, counts, stream=None) -> int:
-        return self.lib.moe_usage_count(self.h, ctypes.byref(cfg.c()), L, T, _ptr(ws),
+        return self.lib.moe_usage_count(self.h, cfg.ref(), L, T, _ptr(ws),
                                         ws.numel() * ws.element_size(), _ptr(counts), _stream(stream))
 
     def usage_count(self, cfg, L, T, ws, counts, stream=None) -> None:
@@ -284,7 +297,7 @@ class Context:
         b = np.ascontiguousarray(b, dtype=np.int32)
         if a.shape != b.shape or a.ndim != 1:
             return EINVAL
-        return self.lib.moe_slot_swap(self.h, ctypes.byref(cfg.c()), _ptr(pool), stride, _ptr(slot_of),
+        return self.lib.moe_slot_swap(self.h, cfg.ref(), _ptr(pool), stride, _ptr(slot_of),
                                       slot_of.numel(), n_slots, a.ctypes.data, b.ctypes.data, a.size,
                                       _stream(stream))
 
@@ -307,7 +320,7 @@ class Context:
 
     # -- the router's balance loss -------------------------------------------------
     def balance_loss_status(self, cfg, logits, idx, mask, T, stats, counts, prob, ws, stream=None) -> int:
-        return self.lib.moe_balance_loss(self.h, ctypes.byref(cfg.c()), _adr(logits), _adr(idx), _adr(mask), T,
+        return self.lib.moe_balance_loss(self.h, cfg.ref(), _adr(logits), _adr(idx), _adr(mask), T,
                                          _adr(stats), _adr(counts), _adr(prob), _adr(ws),
                                          0 if ws is None else ws.nbytes, self._raw_stream(stream))
 
@@ -320,7 +333,7 @@ class Context:
 
     def balance_loss_backward_status(self, cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate, d_logits,
                                      stream=None) -> int:
-        return self.lib.moe_balance_loss_backward(self.h, ctypes.byref(cfg.c()), _adr(logits), _adr(idx), _adr(gate),
+        return self.lib.moe_balance_loss_backward(self.h, cfg.ref(), _adr(logits), _adr(idx), _adr(gate),
                                                   _adr(mask), T, _adr(stats), _adr(counts), _adr(d_loss),
                                                   _adr(d_gate), _adr(d_logits), self._raw_stream(stream))
 
@@ -409,10 +422,10 @@ class Context:
         r = Routing()
         nbytes = ws.numel() * ws.element_size()
         if stack_layers is None:
-            _check(self.lib.moe_layer_routing(ctypes.byref(cfg.c()), T, _ptr(ws), nbytes, ctypes.byref(r)),
+            _check(self.lib.moe_layer_routing(cfg.ref(), T, _ptr(ws), nbytes, ctypes.byref(r)),
                    "moe_layer_routing")
         else:
-            _check(self.lib.moe_stack_routing(ctypes.byref(cfg.c()), stack_layers, T, _ptr(ws), nbytes, layer,
+            _check(self.lib.moe_stack_routing(cfg.ref(), stack_layers, T, _ptr(ws), nbytes, layer,
                                               ctypes.byref(r)), "moe_stack_routing")
         raw = ws.view(torch.uint8).view(-1)
         base = ws.data_ptr()
@@ -592,7 +605,7 @@ class Mx4Matrix:
 
 def balance_workspace(cfg: LayerCfg, device="cuda"):
     import torch
-    n = int(load_library().moe_balance_workspace_bytes(ctypes.byref(cfg.c())))
+    n = int(load_library().moe_balance_workspace_bytes(cfg.ref()))
     if n == 0:
         raise MoeError(EINVAL, "moe_balance_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -608,7 +621,7 @@ def workspace(cfg: LayerCfg, T: int, device="cuda"):
 
 def stack_workspace(cfg: LayerCfg, L: int, T: int, device="cuda"):
     import torch
-    n = int(load_library().moe_stack_workspace_bytes(ctypes.byref(cfg.c()), L, T))
+    n = int(load_library().moe_stack_workspace_bytes(cfg.ref(), L, T))
     if n == 0:
         raise MoeError(EINVAL, "moe_stack_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=device)
