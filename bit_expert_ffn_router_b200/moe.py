@@ -202,7 +202,12 @@ class Context:
         _check(self.lib.moe_ctx_create(device, ctypes.byref(h)), "moe_ctx_create")
         self.h = h
         self.device = device
-        self._current = None  # of a device: its current stream's handle
+        self._bind_torch()
+
+    def _bind_torch(self):
+        import torch
+        self._current = torch._C._cuda_getCurrentRawStream  # of a device: its current stream's handle
+        self._f32, self._i32 = torch.float32, torch.int32
 
     def close(self):
         if self.h:
@@ -311,36 +316,69 @@ class Context:
 
     def _raw_stream(self, stream) -> int:
         """The stream's handle; None is the current stream of this context's device."""
-        if stream is not None:
-            return stream.cuda_stream
-        if self._current is None:
-            import torch
-            self._current = torch._C._cuda_getCurrentRawStream
-        return self._current(self.device)
+        return self._current(self.device) if stream is None else stream.cuda_stream
 
     # -- the router's balance loss -------------------------------------------------
+    # Every tensor has to hold the elements that the call reads or writes, of their type and one after another. Each
+    # question costs 0.05 us of a call's 5 us on the host, a function for a tensor's as much again; so they are asked
+    # in place, and the device of the first tensor stands for all.
+
     def balance_loss_status(self, cfg, logits, idx, mask, T, stats, counts, prob, ws, stream=None) -> int:
-        return self.lib.moe_balance_loss(self.h, cfg.ref(), _adr(logits), _adr(idx), _adr(mask), T,
-                                         _adr(stats), _adr(counts), _adr(prob), _adr(ws),
-                                         0 if ws is None else ws.nbytes, self._raw_stream(stream))
+        f32, i32, E = self._f32, self._i32, cfg.E
+        try:
+            if (logits.get_device() != self.device
+                    or logits.dtype is not f32 or logits.nbytes < 4 * T * E or not logits.is_contiguous()
+                    or idx.dtype is not i32 or idx.nbytes < 4 * T * cfg.k or not idx.is_contiguous()
+                    or stats.dtype is not f32 or stats.nbytes < 16 or not stats.is_contiguous()
+                    or counts.dtype is not i32 or counts.nbytes < 4 * E or not counts.is_contiguous()
+                    or prob.dtype is not f32 or prob.nbytes < 4 * E or not prob.is_contiguous()
+                    or not ws.is_contiguous()
+                    or mask is not None and not _is_mask(mask, T)):
+                return EINVAL
+            return self.lib.moe_balance_loss(self.h, cfg.ref(), logits.data_ptr(), idx.data_ptr(),
+                                             None if mask is None else mask.data_ptr(), T, stats.data_ptr(),
+                                             counts.data_ptr(), prob.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                             self._raw_stream(stream))
+        except AttributeError:  # no tensor
+            return EINVAL
 
     def balance_loss(self, cfg, logits, idx, mask, T, stats, counts, prob, ws, stream=None) -> None:
         """moe_balance_loss: stats [4] fp32 (balance loss, z loss, tokens that count, largest load), counts [E]
-        int32 and prob [E] fp32 from logits [T, E] fp32, idx [T, k] int32 and mask [T] uint8 or None."""
+        int32 and prob [E] fp32 from logits [T, E] fp32, idx [T, k] int32 and mask [T] of single bytes (uint8,
+        bool) or None; ws: balance_workspace. Tensors are contiguous and on the context's device; they may be
+        longer than that."""
         status = self.balance_loss_status(cfg, logits, idx, mask, T, stats, counts, prob, ws, stream)
         if status:
             raise MoeError(status, "moe_balance_loss")
 
     def balance_loss_backward_status(self, cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate, d_logits,
                                      stream=None) -> int:
-        return self.lib.moe_balance_loss_backward(self.h, cfg.ref(), _adr(logits), _adr(idx), _adr(gate),
-                                                  _adr(mask), T, _adr(stats), _adr(counts), _adr(d_loss),
-                                                  _adr(d_gate), _adr(d_logits), self._raw_stream(stream))
+        f32, i32, E = self._f32, self._i32, cfg.E
+        rows, pairs = 4 * T * E, 4 * T * cfg.k
+        try:
+            if (logits.get_device() != self.device
+                    or logits.dtype is not f32 or logits.nbytes < rows or not logits.is_contiguous()
+                    or d_logits.dtype is not f32 or d_logits.nbytes < rows or not d_logits.is_contiguous()
+                    or idx.dtype is not i32 or idx.nbytes < pairs or not idx.is_contiguous()
+                    or stats.dtype is not f32 or stats.nbytes < 16 or not stats.is_contiguous()
+                    or counts.dtype is not i32 or counts.nbytes < 4 * E or not counts.is_contiguous()
+                    or d_loss.dtype is not f32 or d_loss.nbytes < 8 or not d_loss.is_contiguous()
+                    or d_gate is not None and (
+                        gate.dtype is not f32 or gate.nbytes < pairs or not gate.is_contiguous()
+                        or d_gate.dtype is not f32 or d_gate.nbytes < pairs or not d_gate.is_contiguous())
+                    or mask is not None and not _is_mask(mask, T)):
+                return EINVAL
+            return self.lib.moe_balance_loss_backward(
+                self.h, cfg.ref(), logits.data_ptr(), idx.data_ptr(), None if d_gate is None else gate.data_ptr(),
+                None if mask is None else mask.data_ptr(), T, stats.data_ptr(), counts.data_ptr(), d_loss.data_ptr(),
+                None if d_gate is None else d_gate.data_ptr(), d_logits.data_ptr(), self._raw_stream(stream))
+        except AttributeError:  # no tensor
+            return EINVAL
 
     def balance_loss_backward(self, cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate, d_logits,
                               stream=None) -> None:
         """moe_balance_loss_backward: d_logits [T, E] of d_loss[0] * stats[0] + d_loss[1] * stats[1] and, unless
-        d_gate is None, of the gates [T, k]."""
+        d_gate is None, of the gates [T, k] (both fp32). Tensors as for balance_loss."""
         status = self.balance_loss_backward_status(cfg, logits, idx, gate, mask, T, stats, counts, d_loss, d_gate,
                                                    d_logits, stream)
         if status:
@@ -518,11 +556,11 @@ class PreparedStack:
         _check(self.status(x, bias, y), "moe_stack_forward")
 
 
+def _is_mask(t, T) -> bool:
+    return t.element_size() == 1 and t.nbytes >= T and t.is_contiguous()
+
+
 # ------------------------------------------------------------------ 4-bit MX matrices
-
-def _adr(t):
-    return None if t is None else t.data_ptr()
-
 
 def _rows(t):
     """(rows, cols, elements from row to row) of a 2-D tensor with contiguous rows."""

@@ -1,0 +1,153 @@
+"""What the Python calls of the balance loss and of the MX matrices look at in their tensors before the library gets
+an address (no GPU: a context of the CPU's number, -1, with a library that only takes notes)."""
+import ctypes
+
+import pytest
+import torch
+
+from bit_expert_ffn_router_b200 import moe as M
+
+
+class Notes:
+    """A library whose calls succeed and are counted."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append((name, args)) or M.OK
+
+
+class Stream:
+    cuda_stream = 77
+
+
+def context():
+    c = object.__new__(M.Context)
+    c.lib, c.h, c.device = Notes(), ctypes.c_void_p(), -1
+    c._bind_torch()
+    return c
+
+
+class Elsewhere(torch.Tensor):
+    def get_device(self):
+        return 1
+
+
+def elsewhere(t):
+    return t.as_subclass(Elsewhere)
+
+
+def strided(t):
+    """The same values with a gap after each."""
+    return torch.stack((t, t), -1)[..., 0]
+
+
+def misfits(t):
+    """t in ways that the library would misread: another type, too short, with gaps, no tensor."""
+    yield "wide", t.to(torch.int64 if t.dtype != torch.float32 else torch.float64)
+    yield "half", t.to(torch.float16)
+    yield "short", t.reshape(-1)[:-1]
+    yield "strided", strided(t)
+    yield "numpy", t.numpy()
+    if t.dim() == 2:
+        yield "transposed", t.t().contiguous().t()
+        yield "one row for all", t[:1].expand(t.shape)
+
+
+T, E, k = 6, 16, 3
+
+
+def loss_args(mask=True):
+    return dict(logits=torch.randn(T, E), idx=torch.zeros(T, k, dtype=torch.int32),
+                mask=torch.ones(T, dtype=torch.uint8) if mask else None, T=T, stats=torch.zeros(4),
+                counts=torch.zeros(E, dtype=torch.int32), prob=torch.zeros(E), ws=torch.zeros(4096, dtype=torch.uint8))
+
+
+def grad_args(gates=True, mask=True):
+    a = loss_args(mask)
+    return dict(logits=a["logits"], idx=a["idx"], gate=torch.rand(T, k) if gates else None, mask=a["mask"], T=T,
+                stats=a["stats"], counts=a["counts"], d_loss=torch.ones(2), d_gate=torch.rand(T, k) if gates else None,
+                d_logits=torch.zeros(T, E))
+
+
+CFG = M.LayerCfg(d=256, f=128, E=E, k=k)
+CALLS = {"balance_loss": loss_args, "balance_loss_backward": grad_args}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_balance_calls_take_what_fits(call):
+    c = context()
+    for kw in ({}, {"mask": False}):
+        a = CALLS[call](**kw)
+        getattr(c, call)(CFG, **a, stream=Stream)
+        args = c.lib.calls.pop()[1]
+        for n, t in a.items():
+            if isinstance(t, torch.Tensor):
+                assert t.data_ptr() in args, n
+        assert 77 in args and (None in args) == bool(kw)
+    a = CALLS[call]()
+    # longer than needed, of any shape; a mask of any single-byte type
+    for n in set(a) - {"T"}:
+        a[n] = torch.cat((a[n].reshape(-1), a[n].reshape(-1)))
+    for t in (torch.bool, torch.int8):
+        a["mask"] = a["mask"].to(t)
+        getattr(c, call)(CFG, **a, stream=Stream)
+    # no tokens: tensors without elements
+    a = CALLS[call]()
+    a["T"] = 0
+    for n in ("logits", "idx", "mask", "gate", "d_gate", "d_logits"):
+        if n in a:
+            a[n] = a[n][:0]
+    getattr(c, call)(CFG, **a, stream=Stream)
+    assert len(c.lib.calls) == 3
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c in CALLS for n in CALLS[c]() if n not in ("T", "ws")])
+def test_balance_calls_refuse_what_does_not(call, name):
+    c = context()
+    good = CALLS[call]()
+    for what, t in misfits(good[name]):
+        with pytest.raises(M.MoeError) as e:
+            getattr(c, call)(CFG, **{**good, name: t}, stream=Stream)
+        assert e.value.status == M.EINVAL, what
+    if name not in ("mask", "gate", "d_gate"):
+        with pytest.raises(M.MoeError):
+            getattr(c, call)(CFG, **{**good, name: None}, stream=Stream)
+    assert not c.lib.calls
+
+
+def test_balance_workspace_and_gates():
+    c = context()
+    a = loss_args()
+    for ws in (strided(a["ws"]), None):
+        with pytest.raises(M.MoeError):
+            c.balance_loss(CFG, **{**a, "ws": ws}, stream=Stream)
+    with pytest.raises(M.MoeError):  # gates are needed for their gradient
+        c.balance_loss_backward(CFG, **{**grad_args(), "gate": None}, stream=Stream)
+    assert not c.lib.calls
+    c.balance_loss_backward(CFG, **grad_args(gates=False), stream=Stream)
+    c.balance_loss_backward(CFG, **{**grad_args(), "d_gate": None}, stream=Stream)
+    assert len(c.lib.calls) == 2
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_logits_of_another_device_are_refused(call):
+    c, a = context(), CALLS[call]()
+    a["logits"] = elsewhere(a["logits"])
+    with pytest.raises(M.MoeError):
+        getattr(c, call)(CFG, **a, stream=Stream)
+    c.device = 0  # the others' are then the CPU's
+    with pytest.raises(M.MoeError):
+        getattr(c, call)(CFG, **CALLS[call](), stream=Stream)
+    assert not c.lib.calls
+
+
+def test_indices_as_torch_gives_them_are_refused():
+    c = context()
+    a = loss_args()
+    a["idx"] = a["logits"].topk(k, 1)[1]
+    assert a["idx"].dtype == torch.int64
+    assert c.balance_loss_status(CFG, **a, stream=Stream) == M.EINVAL
+    a["idx"] = a["idx"].to(torch.int32)
+    assert c.balance_loss_status(CFG, **a, stream=Stream) == M.OK
