@@ -208,6 +208,7 @@ class Context:
         import torch
         self._current = torch._C._cuda_getCurrentRawStream  # of a device: its current stream's handle
         self._f32, self._i32 = torch.float32, torch.int32
+        self._type_code = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}.get
 
     def close(self):
         if self.h:
@@ -385,11 +386,13 @@ class Context:
             raise MoeError(status, "moe_balance_loss_backward")
 
     # -- 4-bit experts in the MX format ----------------------------------------------
+    # As above: the device of the rows (and of the matrices) stands for their codes' and scales'.
+
     def mx4_quantize_status(self, x, codes, scales, stream=None) -> int:
         rows, cols, ld = _rows(x)
-        if _bad_mx4(codes, scales, rows, cols):
+        if x.get_device() != self.device or _bad_mx4(codes, scales, rows, cols):
             return EINVAL
-        return self.lib.moe_mx4_quantize(self.h, x.data_ptr(), _type_code(x.dtype, -1), rows, cols, ld,
+        return self.lib.moe_mx4_quantize(self.h, x.data_ptr(), self._type_code(x.dtype, -1), rows, cols, ld,
                                          codes.data_ptr(), scales.data_ptr(), self._raw_stream(stream))
 
     def mx4_quantize(self, x, codes, scales, stream=None) -> None:
@@ -401,10 +404,10 @@ class Context:
 
     def mx4_dequantize_status(self, codes, scales, out, stream=None) -> int:
         rows, cols, ld = _rows(out)
-        if _bad_mx4(codes, scales, rows, cols):
+        if out.get_device() != self.device or _bad_mx4(codes, scales, rows, cols):
             return EINVAL
         return self.lib.moe_mx4_dequantize(self.h, codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
-                                           _type_code(out.dtype, -1), ld, self._raw_stream(stream))
+                                           self._type_code(out.dtype, -1), ld, self._raw_stream(stream))
 
     def mx4_dequantize(self, codes, scales, out, stream=None) -> None:
         """moe_mx4_dequantize: the values of codes and scales to out [rows, cols] (bf16, fp16 or fp32)."""
@@ -416,7 +419,8 @@ class Context:
                            swiglu=False, gate=False, stream=None) -> int:
         rows, cols, ld = _rows(out)
         x_rows = codes.shape[0]
-        if _bad_mx4(codes, scales, x_rows, w.cols) or cols != (w.rows // 2 if swiglu else w.rows):
+        if (out.get_device() != self.device or w.device != self.device or _bad_mx4(codes, scales, x_rows, w.cols)
+                or cols != (w.rows // 2 if swiglu else w.rows)):
             return EINVAL
         if grouping is None:
             need, g = x_rows, None
@@ -426,7 +430,7 @@ class Context:
             return EINVAL
         flags = (MX4_GATHER if gather else 0) | (MX4_SWIGLU if swiglu else 0) | (MX4_GATE if gate else 0)
         return self.lib.moe_mx4_product(self.h, codes.data_ptr(), scales.data_ptr(), x_rows, w.ref, g, shared_slot,
-                                        flags, out.data_ptr(), _type_code(out.dtype, -1), ld, self._raw_stream(stream))
+                                        flags, out.data_ptr(), self._type_code(out.dtype, -1), ld, self._raw_stream(stream))
 
     def mx4_product(self, codes, scales, w: "Mx4Matrix", out, grouping=None, shared_slot=-1, gather=False,
                     swiglu=False, gate=False, stream=None) -> None:
@@ -574,14 +578,6 @@ def _rows(t):
     raise MoeError(EINVAL, f"a 2-D tensor with contiguous rows is needed, got {tuple(shape)}, {stride}")
 
 
-def _type_code(dtype, default):
-    """The library's number of a torch dtype; filled in, and replaced by the table's own look-up, on first use."""
-    global _type_code
-    import torch
-    _type_code = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}.get
-    return _type_code(dtype, default)
-
-
 def _bad_mx4(codes, scales, rows, cols) -> bool:
     """Whether codes and scales are not the contiguous bytes of [rows, cols] MX rows (a number of columns
     that no MX row has is left to the library to refuse)."""
@@ -630,7 +626,9 @@ class Mx4Matrix:
         for t, n in ((codes, cols // 2), (scales, pitch)):
             if t.element_size() != 1 or tuple(t.shape) != (self.n_slots, self.rows, n) or not t[0].is_contiguous():
                 raise MoeError(EINVAL, f"Mx4Matrix: a part of shape {tuple(t.shape)} for {cols} columns")
-        self.codes, self.scales = codes, scales
+        if codes.get_device() != scales.get_device():
+            raise MoeError(EINVAL, "Mx4Matrix: codes and scales on two devices")
+        self.codes, self.scales, self.device = codes, scales, codes.get_device()
         self._c = _Mx4(codes.data_ptr(), scales.data_ptr(), codes.stride(0), scales.stride(0), self.n_slots, self.rows,
                        cols)
         self.ref = ctypes.byref(self._c)

@@ -151,3 +151,28 @@ def test_indices_as_torch_gives_them_are_refused():
     assert c.balance_loss_status(CFG, **a, stream=Stream) == M.EINVAL
     a["idx"] = a["idx"].to(torch.int32)
     assert c.balance_loss_status(CFG, **a, stream=Stream) == M.OK
+
+
+def mx(rows, cols):
+    codes, scales = M.mx4_buffers(rows, cols, device="cpu")
+    return codes.zero_(), scales.zero_()
+
+
+def test_mx_rows_of_another_device_are_refused():
+    c = context()
+    x, out = torch.randn(5, 64), torch.zeros(5, 32)
+    w, q = M.Mx4Matrix(*mx(32, 64), 64), mx(5, 64)
+    calls = [lambda e: c.mx4_quantize(e(x), *q, stream=Stream), lambda e: c.mx4_dequantize(*q, e(x), stream=Stream),
+             lambda e: c.mx4_product(*q, w, e(out), stream=Stream)]
+    for f in calls:
+        f(lambda t: t)
+        with pytest.raises(M.MoeError):
+            f(elsewhere)
+    there = M.Mx4Matrix(*map(elsewhere, mx(32, 64)), 64)
+    assert there.device == 1 and w.device == -1
+    with pytest.raises(M.MoeError):
+        c.mx4_product(*q, there, out, stream=Stream)
+    codes, scales = mx(32, 64)
+    with pytest.raises(M.MoeError):
+        M.Mx4Matrix(codes, elsewhere(scales), 64)
+    assert [n for n, _ in c.lib.calls] == ["moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_product"]
