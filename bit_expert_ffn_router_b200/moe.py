@@ -445,8 +445,11 @@ class Context:
         rows with SwiGLU (up: [slots, 2f, d], row 2c gate and 2c + 1 up of channel c), the hidden rows
         quantised, down rows (down: [slots, d, f]) times the gates, to z_rows [n_rows, d] fp32 for combine.
         shared_slot: the pool slot of the shared expert (-1 where cfg.n_shared is 0); bufs: mx4_ffn_buffers."""
-        if (shared_slot >= 0) != bool(cfg.n_shared) or (up.rows, up.cols, down.rows, down.cols) != (
-                2 * cfg.f, cfg.d, cfg.d, cfg.f):
+        # combine reads z_rows by its address alone
+        if ((shared_slot >= 0) != bool(cfg.n_shared)
+                or (up.rows, up.cols, down.rows, down.cols) != (2 * cfg.f, cfg.d, cfg.d, cfg.f)
+                or z_rows.dtype is not self._f32 or not z_rows.is_contiguous()
+                or z_rows.nbytes < 4 * cfg.d * (grouping.n_pairs + (grouping.T if shared_slot >= 0 else 0))):
             raise MoeError(EINVAL, "expert_ffn_mx4")
         xq, h, hq = bufs
         self.mx4_quantize(x, *xq, stream=stream)

@@ -176,3 +176,29 @@ def test_mx_rows_of_another_device_are_refused():
     with pytest.raises(M.MoeError):
         M.Mx4Matrix(codes, elsewhere(scales), 64)
     assert [n for n, _ in c.lib.calls] == ["moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_product"]
+
+
+@pytest.mark.parametrize("n_shared", [0, 1])
+def test_ffn_rows_that_combine_would_misread_are_refused(n_shared):
+    c = context()
+    T, k, d, f, slots = 4, 2, 256, 128, 3
+    cfg = M.LayerCfg(d=d, f=f, E=8, k=k, n_shared=n_shared)
+    g = M.Grouping()
+    g.T, g.k, g.E, g.n_pairs = T, k, 8, T * k
+    n = T * (k + n_shared)
+
+    def pool(rows, cols):
+        q, s = mx(slots * rows, cols)
+        return M.Mx4Matrix(q.view(slots, rows, -1), s.view(slots, rows, -1), cols)
+
+    up, down, bufs = pool(2 * f, d), pool(d, f), M.mx4_ffn_buffers(cfg, T, device="cpu")
+    x, shared = torch.randn(T, d), 2 if n_shared else -1
+    call = lambda z: c.expert_ffn_mx4(cfg, x, g, up, down, shared, bufs, z, stream=Stream)  # noqa: E731
+    call(torch.zeros(n, d))
+    assert [name for name, _ in c.lib.calls] == ["moe_mx4_quantize", "moe_mx4_product"] * 2
+    del c.lib.calls[:]
+    z = torch.zeros(n, d)
+    for bad in (z.bfloat16(), z.half(), z.double(), z[:n - 1], torch.zeros(n, d + 8)[:, :d], torch.zeros(2 * n, d)[::2]):
+        with pytest.raises(M.MoeError):
+            call(bad)
+    assert not c.lib.calls  # refused before anything ran
