@@ -184,3 +184,14 @@ def test_matrix_and_buffer_checks():
     assert (w.n_slots, w.rows, w.c().code_stride, w.c().scale_stride) == (3, 16, 1 << 14, 1 << 14)
     with pytest.raises(M.MoeError):
         M._rows(torch.zeros(4, 8).t())
+
+
+def test_balance_token_limit():
+    """2^24 tokens: their number, and the detail t * k + j of a bad choice, stay exact."""
+    t = 1 << 24
+    for n in (t + 1, 2 ** 31 - 1):
+        assert _balance(T=n) == M.EUNSUPPORTED
+        assert _backward(T=n) == M.EUNSUPPORTED
+    # at the limit the next check speaks
+    assert _balance(T=t, ws_bytes=0) == M.ENOSPACE
+    assert _backward(T=t, d_logits=None) == M.EINVAL
