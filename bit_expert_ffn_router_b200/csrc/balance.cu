@@ -23,10 +23,13 @@
 // choices loaded where they are used: forward 38 against 31 us, backward 55
 // against 48 us at 65521 tokens x 512 experts).
 //
-// Bound by memory, the forward pass by its instructions too (65% of the issue
-// slots): 65521 x 512 forward 31 us (134 MB, 4.3 TB/s), backward 48 us (268 MB,
-// 5.6 TB/s), x 1024 53 and 89 us (5.1, 6.0 TB/s); at 8192 x 512 (12 and 9 us) by the two launches and the
-// two reductions of the forward pass.
+// What bounds it, at 65521 x 512: neither unit is full. The rows' kernel forward
+// takes 28 us of the pass's 32 (137 MB, 4.9 TB/s: DRAM 62%, issue slots 68%), the
+// backward kernel 47 us (276 MB, 5.8 TB/s: 58% and 64%). A row that does not
+// count saves its bytes but not its instructions: with 20% masked forward 30 us
+// (110 MB), backward 46 (247 MB). x 1024: 54 and 90 us (5.0 and 6.0 TB/s). At
+// 8192 x 512 (13 and 11 us) the start of two launches and the two reductions of
+// the forward pass.
 //
 // Sums over tokens: a lane adds its own experts' p over its rows in fp32 (T /
 // 3552 of them at 512 experts), the CTA adds its lane groups in a fixed order, and the finish
@@ -521,12 +524,17 @@ __global__ void __launch_bounds__(row_threads(SLOTS, false))
 
 bool rows_vec(const void* p, int E) { return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Lanes of a row and float4 per lane, and whether rows are float4s. A row has
-// few lanes and many values each, so that its shuffles and choices are shared
-// by more rows of the warp: 65521 x 128 forward 22 us with 32 lanes, 14 with 8,
-// backward 33 and 15; 65521 x 64 with 16 and 8 lanes 14.5 and 11.8, 17.5 and
-// 10.7. Where there is at most one row per warp, its time alone counts and more
-// lanes are faster: 300 x 128 backward 3.8 with 32 lanes, 5.2 with 8.
+// Lanes of a row. With few lanes and many values each, a row's shuffles and
+// choices are shared by more rows of the warp: 65521 x 128 forward 22 us with 32
+// lanes, 14 with 8, backward 33 and 15; 65521 x 64 with 16 and 8 lanes 14.5 and
+// 11.8, 17.5 and 10.7. Where a warp has one row at most (3552 on 148 SMs), its
+// time alone counts and more lanes are faster. Forward + backward with 8 or 16
+// lanes against 32: 300 x 128 7.2 + 5.2 and 7.4 + 3.3 us; at 3552 rows x 128 9.5 +
+// 5.3 and 8.2 + 3.5, x 256 10.3 + 5.6 and 8.7 + 3.9; just past them, at 4200, x 80
+// 8.9 + 5.0 and 9.5 + 4.7, x 128 9.1 + 5.3 and 9.4 + 4.7, x 256 10.5 + 5.5 and 9.3 +
+// 5.3; at 8192 x 128 10.2 + 5.4 and 10.7 + 6.0, x 256 10.8 + 8.2 and 10.9 + 7.0; at
+// 20000 x 128 10.2 + 7.8 and 12.0 + 10.1, x 256 11.6 + 10.7 and 13.5 + 11.3. So 256
+// experts would gain by a border nearer 12000 rows, by 1.4 us at most.
 int lanes_of(const Ctx& ctx, int E, int T) {
   if (E <= 16) return 4;
   if (E <= 64) return 8;
@@ -554,7 +562,9 @@ cudaError_t by_experts(int E, int lanes_per_row, bool vec, F f) {
 }
 
 // One CTA while each of its lane groups has at most kOneCta rows, else up to
-// one per SM.
+// one per SM and the finish. One CTA against several, forward: at 3 rows a group
+// 5.0 and 6.9 us (16 experts), 7.2 and 8.8 (512), 7.8 and 8.9 (1024); at 4 rows 5.7 and
+// 6.5, 8.2 and 8.7, 9.0 and 8.9; at 6 rows 7.0 and 7.5, 10.1 and 8.3, 11.3 and 8.9.
 constexpr int kOneCta = 4;
 
 int balance_ctas(const Ctx& ctx, int E, int lanes, int T) {
