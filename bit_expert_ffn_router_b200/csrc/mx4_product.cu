@@ -33,22 +33,28 @@
 //
 // What bounds it. With few rows per expert, the weights: 64 tokens over 512
 // experts read 613 MB in 91 us. Down products are written at the memory's pace
-// (8192 tokens x 10 experts + shared: 1.19 GB in 203 us, 5.9 TB/s). One matrix
-// with many rows: the way from L2 (40 KB a stage in about 400 ns on every SM, 15
-// TB/s; 7696 x 1536 x 8192 in 62 us, 3.1 PFLOP/s). Gate/up of 8192 tokens takes
-// 229 us for 1.0 GB (155 us): of a stage's 530 ns about 35 are the gathered rows
-// (16-byte copies by the load-store units, again for each of the 8 weight tiles),
-// 30 the epilogue, 210 the MMAs, and the rest the way of codes and scales
-// through the ring. Where the rows follow each other, 16 experts' worth takes 82
-// us (3.6 PFLOP/s), gathered 96.
+// (8192 tokens x 10 experts + shared: 1.19 GB in 203 us, 5.9 TB/s). Elsewhere no
+// unit is full, and the ring is what is waited for: a stage's way round it takes
+// 400 to 530 ns, its MMAs 210, and there are four. Counters:
+//   gate/up, 8192 tokens, 512 experts   228 us  L2 to SM 2.50 GB (11.0 TB/s, L2 45%)  tensor 43%  DRAM 55%
+//   gate/up, 7919 tokens, 16 experts     98 us           1.11 GB (11.3 TB/s,    41%)         39%       13%
+//   7696 x 1536 x 8192, one matrix       67 us           0.72 GB (10.8 TB/s,    36%)         35%        8%
+//   8190 x 1536 x 2048, one matrix       24 us           0.18 GB ( 7.8 TB/s,    24%)         25%        5%
+// In the last, 3.46 waves of tiles take the time of 4: 4 items x 8 stages x 400 ns
+// are 13 us; the other 11 are the launch, the table, the first fill and the last
+// epilogue, which have not been told apart. In gate/up of 8192 tokens about 35 ns
+// of a stage's 530 are the gathered rows (16-byte copies by the load-store units,
+// again for each of the 8 weight tiles) and 30 the epilogue. Where the rows follow
+// each other, 16 experts' worth takes 82 us (3.6 PFLOP/s), gathered 96.
 //
-// Tried and no faster for gate/up: a pair of CTAs on one tile (cta_group::2: half
+// Tried and no faster for gate/up of 8192 tokens over 512 experts, about 160 rows
+// each and gathered (other cases were not tried): a pair of CTAs on one tile (cta_group::2: half
 // the weight traffic, but a stage waits for both, 266 us), x rows that stay for
 // all weight tiles of their row tile (three stages of weight rows are left: 238
 // us), scale copies in a warp of their own (their completion lands behind the
 // MMAs in the queue: 309 against 248 us), a gather warp per stage (372 us), twice
-// the gather warps, a fifth stage, 128 weight rows per tile with a stage more (277
-// us), one arrival per warp a stage late (260 us).
+// the gather warps, 128 weight rows per tile with a stage more (277 us), one
+// arrival per warp a stage late (260 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -78,6 +84,7 @@ constexpr int kPieces = (kBN + 127) / 128;    // of 128 weight rows
 constexpr int kSfCols = 8 + 8 * kPieces;      // TMEM columns of a stage's scales
 constexpr int kGatherRows = kBM / (kGatherThreads / 8);  // rows of a stage per gather thread
 static_assert(2 * kAcc + kStages * kSfCols <= 512, "tensor memory budget");
+static_assert(kScaleParts == 1 + kPieces, "a part for the x rows' scales and one for each piece of weight rows");
 
 // The groups' row tiles, laid end to end: group i's first is prefix[i].
 struct Table {
@@ -99,7 +106,7 @@ struct Table {
 };
 
 // Shared memory: the stages, the epilogue's staging, the table. (A fifth stage
-// in the place of the staging, which gate/up in 16 bits does not need: no faster.)
+// does not fit beside the table, in the place of the staging either.)
 struct Smem {
   // within a stage
   static constexpr int kX = 0;                 // kBM rows x 128 bytes, 128B-swizzled
@@ -601,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < kWarpEpi) {
     // ---------------------------------------------------------- scales
-    // The first warp: the x rows'; the others: weight rows 0 .. 127, 128 .. 255.
+    // Part 0: the x rows'; part 1 and 2: weight rows 0 .. 127 and 128 .. 191 (a piece
+    // has 128, the last 64 repeat the matrix's last row or hold the next tile's: not read).
     // Lane l loads the scales of rows l, l + 32, l + 64, l + 96 for 16 K blocks
     // (two stages) and stores, for each piece of 4 blocks, the four rows' words
     // side by side.
@@ -637,7 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint4 next[4];
     auto load = [&](int pair) {
-      if (part > kPieces) return;
 #pragma unroll
       for (int j = 0; j < 4; ++j) next[j] = ld_plain(reinterpret_cast<const uint4*>(rows[j]) + pair);
     };
@@ -681,17 +688,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        if (part <= kPieces) {
-          uint8_t* stage = smem + st * Smem::kStage;
-          uint4* p0 = reinterpret_cast<uint4*>(stage + (part == 0 ? Smem::kSfX : Smem::kSfW + 512 * (part - 1))) + lane;
-          uint4* p1 = p0 + (part == 0 ? 512 : 512 * kPieces) / 16;
-          if (s == 0) {
-            *p0 = make_uint4(cur[0].x, cur[1].x, cur[2].x, cur[3].x);
-            *p1 = make_uint4(cur[0].y, cur[1].y, cur[2].y, cur[3].y);
-          } else {
-            *p0 = make_uint4(cur[0].z, cur[1].z, cur[2].z, cur[3].z);
-            *p1 = make_uint4(cur[0].w, cur[1].w, cur[2].w, cur[3].w);
-          }
+        uint8_t* stage = smem + st * Smem::kStage;
+        uint4* p0 = reinterpret_cast<uint4*>(stage + (part == 0 ? Smem::kSfX : Smem::kSfW + 512 * (part - 1))) + lane;
+        uint4* p1 = p0 + (part == 0 ? 512 : 512 * kPieces) / 16;
+        if (s == 0) {
+          *p0 = make_uint4(cur[0].x, cur[1].x, cur[2].x, cur[3].x);
+          *p1 = make_uint4(cur[0].y, cur[1].y, cur[2].y, cur[3].y);
+        } else {
+          *p0 = make_uint4(cur[0].z, cur[1].z, cur[2].z, cur[3].z);
+          *p1 = make_uint4(cur[0].w, cur[1].w, cur[2].w, cur[3].w);
         }
         // the gathered rows' writes are announced with this warp's own
         if (part == 0 && P.gather && !wait_warp(B, &B->x_full[st], (g / kStages) & 1, P, 7)) {
@@ -858,7 +863,7 @@ cudaError_t launch_mx4_product(const Ctx& ctx, const Mx4Args& a, cudaStream_t s)
   P.n_slots = a.w.n_slots;
   P.K = a.w.cols;
   P.pitch = mx4_pitch(a.w.cols);
-    P.grouped = a.g != nullptr;
+  P.grouped = a.g != nullptr;
   long long groups = 1, rows = a.x_rows;  // at most
   if (a.g != nullptr) {
     P.n_uniq = a.g->n_uniq;
