@@ -26,10 +26,10 @@
 // What bounds it, at 65521 x 512: neither unit is full. The rows' kernel forward
 // takes 28 us of the pass's 32 (137 MB, 4.9 TB/s: DRAM 62%, issue slots 68%), the
 // backward kernel 47 us (276 MB, 5.8 TB/s: 58% and 64%). A row that does not
-// count saves its bytes but not its instructions: with 20% masked forward 30 us
-// (110 MB), backward 46 (247 MB). x 1024: 54 and 90 us (5.0 and 6.0 TB/s). At
-// 8192 x 512 (13 and 11 us) the start of two launches and the two reductions of
-// the forward pass.
+// count saves its bytes but not its instructions: with none, 20% and 50% masked
+// 32, 31 and 29 us forward, 48, 46 and 42 backward. x 1024: 54 and 90 us (5.0 and 6.0
+// TB/s). At 8192 x 512 (13 and 10 us) the start of two launches and the two
+// reductions of the forward pass.
 //
 // Sums over tokens: a lane adds its own experts' p over its rows in fp32 (T /
 // 3552 of them at 512 experts), the CTA adds its lane groups in a fixed order, and the finish

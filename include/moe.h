@@ -397,7 +397,8 @@ MOE_API moe_status moe_layer_forward_static(moe_ctx* ctx, const moe_layer_cfg* c
  *   stats[1]  = sum_t (log sum_e exp logits[t, e])^2 / n         (the z loss)
  *   stats[2]  = n
  *   stats[3]  = E / (k n) * max_e counts[e]             (1 for an even router)
- * and all of them 0 where n = 0 (T = 0 among them). T <= 2^24. logits [T, E] fp32 and
+ * and all of them 0 where n = 0 (T = 0 among them: logits, idx and mask are not
+ * looked at then). T <= 2^24. logits [T, E] fp32 and
  * idx [T, k] int32 as moe_router_topk gives them (the bias included); mask
  * [T] bytes or NULL; stats [4], prob [E] fp32, counts [E] int32 out. Sums over
  * tokens are taken in a fixed order: equal calls give equal bits. An idx
@@ -468,7 +469,8 @@ typedef struct {
 } moe_mx4_matrix;
 
 #define MOE_MX4_GATHER 1 /* x holds one row per token, not per output row */
-#define MOE_MX4_SWIGLU 2 /* w's rows 2c, 2c+1 are gate and up row of channel c: out = silu(gate) * up */
+#define MOE_MX4_SWIGLU 2 /* w's rows 2c, 2c+1 are gate and up row of channel c: out = silu(gate) * up,
+                          * with silu below 2^-119 in magnitude (gate < -87) taken as 0 */
 #define MOE_MX4_GATE   4 /* output rows of pairs are multiplied by pair_gate */
 
 /* out = x w^T on 4-bit codes, sums in fp32, rounded once to out_type.
