@@ -1,4 +1,5 @@
-"""ctypes binding of libmoe (include/moe.h): argument marshalling only.
+"""ctypes binding of libmoe (include/moe.h): argument marshalling, and for the
+balance loss and the MX calls a look at their tensors.
 
 Every step of the MoE FFN runs inside libmoe's CUDA kernels; this module turns
 torch tensors into device pointers and the current torch stream into a
